@@ -16,18 +16,14 @@
 #include <vector>
 
 #include "../../include/mps_adamw.h"
+#include "errors.h"
 #include "kernels.h"
 #include "layout.h"
 
+namespace mps {
 namespace {
-
-using mps::TensorEntry;
-using mps::WorkspaceHeader;
-
-static_assert(mps::kScratchBytes == MPS_NOALLOC_WORKSPACE_BYTES,
-              "the header states the library-held workspace's size");
-
 thread_local std::string g_last_error;
+}
 
 int fail(int code, const char* fmt, ...)
 {
@@ -45,6 +41,17 @@ int ok()
     g_last_error.clear();
     return MPS_OK;
 }
+}  // namespace mps
+
+namespace {
+
+using mps::fail;
+using mps::ok;
+using mps::TensorEntry;
+using mps::WorkspaceHeader;
+
+static_assert(mps::kScratchBytes == MPS_NOALLOC_WORKSPACE_BYTES,
+              "the header states the library-held workspace's size");
 
 // ------------------------------------------------------------ the plan ---
 
@@ -975,6 +982,6 @@ int adamw8_dequantize(const uint8_t* d_codes, const uint8_t* d_scales, int64_t n
     return ok();
 }
 
-const char* adamw_last_error(void) { return g_last_error.c_str(); }
+const char* adamw_last_error(void) { return mps::g_last_error.c_str(); }
 
 }  // extern "C"
