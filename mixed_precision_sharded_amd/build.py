@@ -15,8 +15,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmps_adamw.so")
-SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "kernels_q8.hip"),
-           os.path.join(CSRC, "api.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in (
+    "kernels.hip", "kernels_q8.hip", "kernels_act8.hip", "kernels_wgrad.hip",
+    "kernels_policy.hip", "api.cpp", "train_api.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -2,7 +2,8 @@
 // resources and vector loads/stores, bf16 rounding, fp64 wavefront and block
 // reductions, the norm's second stage, the step counter, the clip
 // multiplier, the step scalars and the per-element update.  Included by
-// kernels.hip and kernels_q8.hip only.
+// kernels.hip and kernels_q8.hip, and by rows.h for the vector types, bf16
+// rounding and the fp64 reductions.
 //
 // Build with -ffp-contract=off: every fp32 operation below must round once,
 // in source order; division and sqrt are the correctly rounded defaults.

@@ -1,0 +1,214 @@
+// Device helpers of the row-matrix operators (8-bit activations, weight
+// gradients, the policy loss): eight consecutive elements of a row at a time,
+// their 8-bit form, and reductions in fp32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "device.h"
+#include "fp8.h"
+
+namespace mps {
+namespace {
+
+constexpr int kRun = 32;   // elements that share a scale byte (MPS_Q8_BLOCK)
+constexpr int kUnit = 8;   // elements a lane takes at a time: four lanes hold a run
+
+// Vectors at any element's address: a global access of 16 bytes needs no
+// alignment on this chip, so rows of any start and stride take one path.
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight elements as they lie in memory.
+template <bool kBf16>
+struct Raw8 {
+    u32x4 v[kBf16 ? 1 : 2];
+};
+
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> load_full(const void* base, int64_t at)
+{
+    Raw8<kBf16> r;
+    if (kBf16) {
+        r.v[0] = *reinterpret_cast<const u32x4_at2*>(static_cast<const uint16_t*>(base) + at);
+    } else {
+        const auto* p = reinterpret_cast<const u32x4_at4*>(static_cast<const float*>(base) + at);
+        r.v[0] = p[0];
+        r.v[kBf16 ? 0 : 1] = p[1];
+    }
+    return r;
+}
+
+// Elements at .. at + 7, of which the first n exist (zeros behind them).
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> load8(const void* base, int64_t at, int64_t n)
+{
+    if (n >= kUnit) return load_full<kBf16>(base, at);
+    Raw8<kBf16> r{};
+    for (int i = 0; i < kUnit - 1; ++i) {
+        if (i >= n) break;
+        if (kBf16) {
+            const uint32_t h = static_cast<const uint16_t*>(base)[at + i];
+            const uint32_t word = (i & 1) ? h << 16 : h;
+            if (i / 2 == 0) r.v[0][0] |= word;
+            else if (i / 2 == 1) r.v[0][1] |= word;
+            else if (i / 2 == 2) r.v[0][2] |= word;
+            else r.v[0][3] |= word;
+        } else {
+            const uint32_t word = static_cast<const uint32_t*>(base)[at + i];
+            constexpr int kHi = kBf16 ? 0 : 1;
+            if (i == 0) r.v[0][0] = word;
+            else if (i == 1) r.v[0][1] = word;
+            else if (i == 2) r.v[0][2] = word;
+            else if (i == 3) r.v[0][3] = word;
+            else if (i == 4) r.v[kHi][0] = word;
+            else if (i == 5) r.v[kHi][1] = word;
+            else r.v[kHi][2] = word;
+        }
+    }
+    return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void widen(const Raw8<kBf16>& r, float (&x)[kUnit])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kBf16) {
+            x[2 * i] = bf16_lo(r.v[0][i]);
+            x[2 * i + 1] = bf16_hi(r.v[0][i]);
+        } else {
+            x[i] = __uint_as_float(r.v[0][i]);
+            x[4 + i] = __uint_as_float(r.v[kBf16 ? 0 : 1][i]);
+        }
+    }
+}
+
+// Round (bf16: to nearest, ties to even) and store the first n of eight.
+template <bool kBf16>
+__device__ __forceinline__ void store8(const float (&x)[kUnit], void* base, int64_t at, int64_t n)
+{
+    if (n >= kUnit) {
+        if (kBf16) {
+            u32x4_at2 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16_pack2(x[2 * i], x[2 * i + 1]);
+            *reinterpret_cast<u32x4_at2*>(static_cast<uint16_t*>(base) + at) = w;
+        } else {
+            auto* p = reinterpret_cast<u32x4_at4*>(static_cast<float*>(base) + at);
+            p[0] = u32x4_at4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+            p[1] = u32x4_at4{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnit - 1; ++i) {
+        if (i >= n) break;
+        if (kBf16) static_cast<uint16_t*>(base)[at + i] = bf16_one(x[i]);
+        else static_cast<float*>(base)[at + i] = x[i];
+    }
+}
+
+// ------------------------------------------------------- the 8-bit form ---
+
+// Largest over the four lanes of a quad (the lanes that hold one run).
+__device__ __forceinline__ uint32_t quad_max(uint32_t x)
+{
+    constexpr int kQuadSwap1 = 0xb1;  // quad_perm [1,0,3,2]
+    constexpr int kQuadSwap2 = 0x4e;  // quad_perm [2,3,0,1]
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), kQuadSwap1, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), kQuadSwap2, 0xf, 0xf, false)));
+    return x;
+}
+
+// Encode this lane's eight elements, the quad's lanes holding one run, and
+// store them as unit `unit` of the matrix (eight codes; the quad's first
+// lane writes the scale byte).  The four lanes come here together.
+__device__ __forceinline__ void store_codes(const float (&x)[kUnit], uint8_t* codes, uint8_t* scales,
+                                            int64_t unit)
+{
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) most = max(most, abs_bits(x[i]));
+    const uint32_t byte = scale_byte<kE4M3TopExp>(quad_max(most));
+    const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
+    reinterpret_cast<u32x2*>(codes)[unit] = u32x2{encode4<true>(lo, byte), encode4<true>(hi, byte)};
+    if (unit % 4 == 0) scales[unit / 4] = static_cast<uint8_t>(byte);
+}
+
+// Eight codes to the values they stand for: the conversion takes 2^(b - 127)
+// as an fp32 scale whose exponent field is b, 0 and 255 (NaN) included.
+__device__ __forceinline__ void decode8(u32x2 c, uint32_t byte, float (&x)[kUnit])
+{
+    const float scale = __uint_as_float(byte << 23);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[i], scale, false);
+        const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[i], scale, true);
+        x[4 * i] = lo[0];
+        x[4 * i + 1] = lo[1];
+        x[4 * i + 2] = hi[0];
+        x[4 * i + 3] = hi[1];
+    }
+}
+
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int64_t unit,
+                                           float (&x)[kUnit])
+{
+    decode8(reinterpret_cast<const u32x2*>(codes)[unit], scales[unit / 4], x);
+}
+
+// ---------------------------------------------------- the walk over rows ---
+
+// The units of a matrix of `rows` rows of `per_row` units, in order, from
+// `first` on and `step` apart: one division at the start, none behind it.
+struct RowWalk {
+    int64_t row, d_row;
+    uint32_t col, d_col, per_row;
+
+    __device__ __forceinline__ RowWalk(int64_t first, int64_t step, uint32_t units_per_row)
+        : per_row(units_per_row)
+    {
+        row = first / units_per_row;
+        col = static_cast<uint32_t>(first - row * units_per_row);
+        d_row = step / units_per_row;
+        d_col = static_cast<uint32_t>(step - d_row * units_per_row);
+    }
+
+    __device__ __forceinline__ void next()
+    {
+        row += d_row;
+        col += d_col;
+        if (col >= per_row) {
+            col -= per_row;
+            ++row;
+        }
+    }
+
+    __device__ __forceinline__ int64_t unit() const { return row * per_row + col; }
+};
+
+// ------------------------------------------------------ reductions (fp32) ---
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp_movef(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), kCtrl, 0xf, 0xf, false));
+}
+
+// Sum over the wavefront, the same bits in every lane; all lanes active.
+__device__ __forceinline__ float wave_sumf(float x)
+{
+    x += dpp_movef<0xb1>(x);
+    x += dpp_movef<0x4e>(x);
+    x += dpp_movef<0x141>(x);
+    x += dpp_movef<0x140>(x);
+    x += __shfl_xor(x, 16, kWave);
+    x += __shfl_xor(x, 32, kWave);
+    return x;
+}
+
+}  // namespace
+}  // namespace mps
