@@ -63,7 +63,7 @@ __device__ __forceinline__ RowResult row_result(const PolicyArgs& a, int64_t row
     if (a.ref_logp) {
         const double d = static_cast<double>(a.ref_logp[row]) - logp;
         const double q = exp(d);
-        const double kl = q - d - 1.0;
+        const double kl = q == INFINITY ? q : q - d - 1.0;  // the label has no probability left
         r.kl = static_cast<float>(kl);
         gain -= a.kl_coef * kl;
         slope += a.kl_coef * (1.0 - q);
