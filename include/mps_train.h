@@ -175,7 +175,8 @@ int act8_weight_grad(const void* d_dy, mps_dtype dy_dtype, int64_t dy_stride,
  * A row is left out (loss, l, kl and gradient 0; its logits are not read)
  * when its label is outside [0, vocab) or its weight is 0, and so is a row
  * whose logits are all -inf.  Single logits of -inf are tokens the
- * vocabulary does not offer; a NaN or +inf logit makes its row NaN.
+ * vocabulary does not offer (a label among them has l = -inf: a ratio of 0
+ * and an infinite KL term); a NaN or +inf logit makes its row NaN.
  *
  *   d_logits, logits_dtype, logits_stride : [rows, vocab].
  *   d_labels     : int64 [rows].

@@ -186,6 +186,197 @@ __global__ __launch_bounds__(kBlock) void weight_grad_kernel(Matrix dy, Codes x,
     }
 }
 
+// ------------------------------------------------------------- wide tiles ---
+//
+// 256 x 256 of dw per block, four wavefronts of 128 x 128 each (256 of a
+// SIMD's 512 registers per lane hold the sums), stages of 64 t, two of them
+// in LDS.  Per stage and wavefront: 64 matrix instructions of 32 cycles; per
+// CU 128 KB read from LDS and 64 KB written, 1536 of those 2048 cycles, so
+// the tile cannot be smaller, and the LDS accesses have to run beside the
+// matrix instructions.  A stage is therefore unrolled into four steps of 16
+// t, and a step's code reads the operands of the next one, moves a share of
+// the next stage from registers to LDS and asks memory for a share of the one
+// after that, all between its own 16 matrix instructions.  The block meets
+// once per stage, before the last step: by then every operand of the stage is
+// in registers and the next stage is in LDS.
+//
+// Rows behind the last token come as zeros of both operands (the buffer
+// resources end with the split's tokens); columns behind the matrix's own
+// read what lies there and are not stored.
+
+constexpr int kWideTile = 256;
+constexpr int kWideT = 64;
+constexpr int kWideRow = kWideTile * 2;             // bytes of a staged row
+constexpr int kWideStage = kWideT * kWideRow;       // bytes of a staged operand
+
+__device__ __forceinline__ uint32_t wide_chunk_at(int t, int chunk)
+{
+    return static_cast<uint32_t>(t * kWideRow + ((chunk ^ ((t & 3) << 2)) << 4));
+}
+
+// Bytes from `from` to `to` that a buffer resource may reach.
+__device__ __forceinline__ uint32_t reach(int64_t bytes)
+{
+    return static_cast<uint32_t>(bytes < 0 ? 0 : (bytes > 0xfffffffcll ? 0xfffffffcll : bytes));
+}
+
+struct WideStage {
+    u32x4 dy[8];     // 64 x 256 bf16, eight chunks of eight per thread
+    u32x4 codes[4];  // 64 x 256 codes, four units of sixteen
+    uint32_t scale[4];
+};
+
+template <bool kDwBf16>
+__global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
+                                                                     int64_t k_all, int64_t per_split, uint32_t tiles_k,
+                                                                     void* dw, bool accumulate, float* partials)
+{
+    __shared__ __attribute__((aligned(16))) char lds[4 * kWideStage];  // dy: two stages, x: two stages
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x / tiles_k) * kWideTile;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x % tiles_k) * kWideTile;
+    const int64_t padded = (k_all + kRun - 1) / kRun * kRun;
+    const int64_t t_first = blockIdx.y * per_split;
+    const int64_t t_last = min(t_first + per_split, tokens);
+    const int stages = static_cast<int>((t_last - t_first + kWideT - 1) / kWideT);
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int wn = wave / 2 * 128, wk = wave % 2 * 128;
+
+    // Where this thread's share of a stage lies, in bytes from the stage's first row.
+    const uint32_t dy_row = static_cast<uint32_t>(dy.stride) * 2u, x_row = static_cast<uint32_t>(padded);
+    const uint32_t dy_off = (tid / 32) * dy_row + (tid % 32) * 16u;     // + 8 rows per chunk
+    const uint32_t x_off = (tid / 16) * x_row + (tid % 16) * 16u;       // + 16 rows per unit
+    const uint32_t s_off = (tid / 16) * (x_row / 32) + (tid % 16) / 2;
+    const char* dy_base = static_cast<const char*>(dy.data) + n0 * 2;
+    const uint8_t* x_base = x.codes + k0;
+    const uint8_t* s_base = x.scales + k0 / kRun;
+
+    auto load_dy = [&](WideStage& w, int s, int first, int count) {
+        const int64_t t0 = t_first + static_cast<int64_t>(s) * kWideT;
+        const __amdgpu_buffer_rsrc_t r = rsrc(dy_base + t0 * dy_row, reach((t_last - t0) * dy_row - (dy.stride - n_all + n0) * 2));
+#pragma unroll
+        for (int j = first; j < first + count; ++j) w.dy[j] = load_u32x4<0>(r, dy_off + j * 8 * dy_row);
+    };
+    auto load_x = [&](WideStage& w, int s, int first, int count) {
+        const int64_t t0 = t_first + static_cast<int64_t>(s) * kWideT;
+        const __amdgpu_buffer_rsrc_t r = rsrc(x_base + t0 * x_row, reach((t_last - t0) * x_row - k0));
+        const __amdgpu_buffer_rsrc_t rs = rsrc(s_base + t0 * (x_row / 32), reach((t_last - t0) * (x_row / 32) - k0 / kRun));
+#pragma unroll
+        for (int j = first; j < first + count; ++j) {
+            w.codes[j] = load_u32x4<0>(r, x_off + j * 16 * x_row);
+            w.scale[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, s_off + j * 16 * (x_row / 32), 0, 0);
+        }
+    };
+    const uint32_t dy_at = wide_chunk_at(tid / 32, tid % 32);              // + 8 rows: the same t & 3
+    const uint32_t x_at = 2 * kWideStage + wide_chunk_at(tid / 16, tid % 16 * 2);  // + 16 rows
+    auto put_dy = [&](const WideStage& w, int buf, int first, int count) {
+#pragma unroll
+        for (int j = first; j < first + count; ++j) *reinterpret_cast<u32x4*>(lds + buf * kWideStage + dy_at + j * 8 * kWideRow) = w.dy[j];
+    };
+    auto put_x = [&](const WideStage& w, int buf, int first, int count) {
+#pragma unroll
+        for (int j = first; j < first + count; ++j) {
+            const float scale = __uint_as_float(w.scale[j] << 23);
+            u32x4 lo, hi;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lo[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][i], scale, false));
+                lo[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][i], scale, true));
+                hi[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][2 + i], scale, false));
+                hi[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][2 + i], scale, true));
+            }
+            // A unit's two chunks differ in the lowest bit only, which the exclusive-or leaves.
+            char* p = lds + buf * kWideStage + x_at + j * 16 * kWideRow;
+            *reinterpret_cast<u32x4*>(p) = lo;
+            *reinterpret_cast<u32x4*>(p + 16) = hi;
+        }
+    };
+    // Operand addresses: column block i of 32 sits at chunk 4 i, whose exclusive-or with the row is the lane's own.
+    uint32_t a_at[4], b_at[4];
+    {
+        const int l16 = lane % 16, t = lane / 32 * 8 + l16 / 4;
+        const int low = lane % 32 / 16 * 2 + l16 % 4 / 2;  // chunk within the 32 columns
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = t * kWideRow + (((i ^ (t & 3)) * 4 + low) << 4) + l16 % 2 * 8;
+            a_at[i] = at + wn * 2;
+            b_at[i] = at + wk * 2 + 2 * kWideStage;
+        }
+    }
+    auto read4 = [&](bf16x8 (&v)[4], const uint32_t (&at)[4], int buf, int step) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char* p = lds + at[i] + buf * kWideStage + step * 16 * kWideRow;
+            const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                             (__attribute__((address_space(3))) s16x4*)p));
+            const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                             (__attribute__((address_space(3))) s16x4*)(p + 4 * kWideRow)));
+            v[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+
+    f32x16 acc[4][4] = {};
+    bf16x8 a[2][4], b[2][4];
+    WideStage w;
+    auto multiply = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
+        }
+    };
+    load_dy(w, 0, 0, 8);
+    load_x(w, 0, 0, 4);
+    put_dy(w, 0, 0, 8);
+    put_x(w, 0, 0, 4);
+    load_dy(w, 1, 0, 8);
+    load_x(w, 1, 0, 4);
+    __syncthreads();
+    read4(a[0], a_at, 0, 0);
+    read4(b[0], b_at, 0, 0);
+    for (int s = 0; s < stages; ++s) {
+        const int buf = s & 1;
+        read4(a[1], a_at, buf, 1);
+        read4(b[1], b_at, buf, 1);
+        put_dy(w, buf ^ 1, 0, 4);
+        put_x(w, buf ^ 1, 0, 1);
+        load_dy(w, s + 2, 0, 4);
+        load_x(w, s + 2, 0, 1);
+        multiply(0);
+        read4(a[0], a_at, buf, 2);
+        read4(b[0], b_at, buf, 2);
+        put_dy(w, buf ^ 1, 4, 4);
+        put_x(w, buf ^ 1, 1, 1);
+        load_dy(w, s + 2, 4, 4);
+        load_x(w, s + 2, 1, 1);
+        multiply(1);
+        read4(a[1], a_at, buf, 3);
+        read4(b[1], b_at, buf, 3);
+        put_x(w, buf ^ 1, 2, 2);
+        load_x(w, s + 2, 2, 2);
+        multiply(0);
+        __syncthreads();
+        read4(a[0], a_at, buf ^ 1, 0);
+        read4(b[0], b_at, buf ^ 1, 0);
+        multiply(1);
+    }
+    float* mine = partials ? partials + static_cast<int64_t>(blockIdx.y) * n_all * k_all : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t k = k0 + wk + j * kFrag + lane % 32;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t n = n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4;
+                if (n < n_all && k < k_all) {
+                    if (mine) mine[n * k_all + k] = acc[i][j][r];
+                    else store_dw<kDwBf16>(dw, n * k_all + k, acc[i][j][r], accumulate);
+                }
+            }
+        }
+    }
+}
+
 // dw = [dw +] the splits' partial sums, in split order.
 template <bool kDwBf16>
 __global__ __launch_bounds__(kBlock) void weight_grad_join_kernel(const float* partials, int splits, int64_t count,
@@ -204,36 +395,67 @@ struct Shape {
     int splits;
 };
 
-// Enough blocks for the chip's 256 CUs, each with at least 16 stages.
-Shape shape_of(int64_t tokens, int64_t n, int64_t k)
+// How the tokens are split: the count of splits under which the slowest CU
+// has least to do, in stages of the tile (`per_cu` blocks run on a CU at
+// once), against the partial sums' way to memory and back.  `stage_us` is a
+// stage's measured time.
+Shape shape_of(int64_t tokens, int64_t n, int64_t k, int tile, int stage_t, int per_cu, double stage_us)
 {
     Shape s;
-    s.tiles_n = (n + kTile - 1) / kTile;
-    s.tiles_k = (k + kTile - 1) / kTile;
+    s.tiles_n = (n + tile - 1) / tile;
+    s.tiles_k = (k + tile - 1) / tile;
     const int64_t tiles = s.tiles_n * s.tiles_k;
-    const int64_t stages = (tokens + kTileT - 1) / kTileT;
-    int64_t splits = 512 / tiles;
-    if (splits > stages / 16) splits = stages / 16;
-    if (splits < 1) splits = 1;
-    const int64_t per = (stages + splits - 1) / splits;
-    s.per_split = per * kTileT;
+    const int64_t stages = (tokens + stage_t - 1) / stage_t;
+    const int64_t slots = 256 * per_cu;
+    const double join_us = 3.0 + static_cast<double>(n) * k * 8.0 / 4.0e6;  // per split: written and read at 4 TB/s
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t c = 1; c <= 32 && (c == 1 || c * 4 <= stages); ++c) {
+        const int64_t rounds = (tiles * c + slots - 1) / slots;
+        const double cost = rounds * ((stages + c - 1) / c + 4) * stage_us + (c > 1 ? 3.0 + c * (join_us - 3.0) : 0.0);
+        if (c == 1 || cost < least) {
+            best = c;
+            least = cost;
+        }
+    }
+    const int64_t per = (stages + best - 1) / best;
+    s.per_split = per * stage_t;
     s.splits = static_cast<int>(per > 0 ? (stages + per - 1) / per : 1);
     return s;
 }
 
+Shape narrow_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kTile, kTileT, 2, 1.2); }
+Shape wide_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kWideTile, kWideT, 1, 2.0); }
+
+// The wide tile takes bf16 gradients whose rows are whole 16-byte chunks.
+bool wide_fits(const Matrix& dy, bool dy_bf16, int64_t tokens, int64_t n, int64_t k)
+{
+    if (!dy_bf16 || n % 8 || dy.stride % 8 || reinterpret_cast<uintptr_t>(dy.data) % 16) return false;
+    if (dy.stride >= 1 << 25) return false;  // a stage's offsets stay below 2^32 bytes
+    return tokens >= 256 && n * k >= 1 << 20;
+}
+
+size_t scratch_of(const Shape& s, int64_t n, int64_t k)
+{
+    return s.splits > 1 ? static_cast<size_t>(s.splits) * n * k * sizeof(float) : 0;
+}
+
 }  // namespace
 
+// Whichever tile the gradient's layout will allow.
 size_t weight_grad_scratch(int64_t tokens, int64_t out_features, int64_t in_features)
 {
-    const Shape s = shape_of(tokens, out_features, in_features);
-    return s.splits > 1 ? static_cast<size_t>(s.splits) * out_features * in_features * sizeof(float) : 0;
+    const size_t narrow = scratch_of(narrow_shape(tokens, out_features, in_features), out_features, in_features);
+    const size_t wide = scratch_of(wide_shape(tokens, out_features, in_features), out_features, in_features);
+    return narrow > wide ? narrow : wide;
 }
 
 hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tokens, int64_t out_features,
                                    int64_t in_features, void* dw, bool dw_bf16, bool accumulate, void* scratch,
                                    hipStream_t stream)
 {
-    const Shape s = shape_of(tokens, out_features, in_features);
+    const bool wide = wide_fits(dy, dy_bf16, tokens, out_features, in_features);
+    const Shape s = wide ? wide_shape(tokens, out_features, in_features) : narrow_shape(tokens, out_features, in_features);
     float* partials = s.splits > 1 ? static_cast<float*>(scratch) : nullptr;
     const dim3 grid(static_cast<uint32_t>(s.tiles_n * s.tiles_k), s.splits);
     const uint32_t tk = static_cast<uint32_t>(s.tiles_k);
@@ -241,7 +463,10 @@ hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tok
         kernel<<<grid, kBlock, 0, stream>>>(dy, x, tokens, out_features, in_features, s.per_split, tk, dw, accumulate,
                                             partials);
     };
-    if (dy_bf16) {
+    if (wide) {
+        if (dw_bf16) run(weight_grad_wide_kernel<true>);
+        else run(weight_grad_wide_kernel<false>);
+    } else if (dy_bf16) {
         if (dw_bf16) run(weight_grad_kernel<true, true>);
         else run(weight_grad_kernel<true, false>);
     } else {

@@ -17,7 +17,9 @@ TYPES = [torch.bfloat16, torch.float32]
 # of stages of 32 and 64 tokens; more tokens than one block takes; none.
 SHAPES = [(1, 1, 1), (5, 3, 7), (31, 33, 32), (32, 128, 128), (33, 129, 131), (64, 64, 256), (65, 256, 96), (0, 40, 50),
           (100, 8, 2051), (257, 513, 40), (515, 1000, 33), (1030, 260, 520), (2500, 72, 136), (4099, 16, 24), (300, 512, 768),
-          (700, 768, 512)]
+          (700, 768, 512),
+          # from here on bf16 gradients take tiles of 256 (where their rows allow it), with edges in every direction
+          (256, 1024, 1024), (257, 1032, 1025), (1030, 520, 2051), (319, 2056, 520), (1500, 264, 4000), (400, 1025, 1030)]
 
 
 def gen(seed):
@@ -53,10 +55,12 @@ def test_whole_numbers_bitwise(oracle_lib, dtype, dw_type, t, n, k):
     x = torch.randint(-4, 5, (t, k), generator=g, device=DEV).float()
     codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, x))
     codes[:, k:] = 0x38
-    wide = torch.randint(-8, 9, (t + 2, n + 5), generator=g, device=DEV).to(dtype)
+    # A matrix inside a larger one: 16-byte rows where n allows them, else an odd start and stride.
+    left = 8 if n % 8 == 0 else 3
+    wide = torch.randint(-8, 9, (t + 2, n + left + 8), generator=g, device=DEV).to(dtype)
     wide[t:] = float("nan")  # rows behind the last token
-    wide[:, n + 2:], wide[:, :2] = float("nan"), float("inf")  # columns beside the matrix
-    dy = wide[:t, 2:n + 2]
+    wide[:, n + left:], wide[:, :left] = float("nan"), float("inf")  # columns beside the matrix
+    dy = wide[:t, left:n + left]
     want, _ = product(dy, codes, scales, k)
     dw, buf = guarded(n, k, dw_type)
     ws = workspace(t, n, k)
@@ -95,9 +99,9 @@ def test_fp32_gradients_keep_all_their_bits(oracle_lib):
     assert torch.equal(dw, dy.t().expand(400, 32))
 
 
-@pytest.mark.parametrize("dtype", TYPES)
-def test_nonfinite_values_stay_in_their_rows_and_columns(oracle_lib, dtype):
-    t, n, k = 70, 150, 160
+@pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 70, 150, 160), (torch.float32, 70, 150, 160),
+                                         (torch.bfloat16, 270, 1032, 1100)])
+def test_nonfinite_values_stay_in_their_rows_and_columns(oracle_lib, dtype, t, n, k):
     x = torch.ones(t, k)
     x[3, 40] = float("nan")  # the run of columns 32 .. 63
     dy = torch.ones(t, n, device=DEV, dtype=dtype)
@@ -125,9 +129,9 @@ def test_small_and_large_kept_values(oracle_lib):
     assert torch.equal(dw.cpu(), x * 2)
 
 
-def test_two_runs_give_the_same_bits(oracle_lib):
+@pytest.mark.parametrize("t,n,k", [(5000, 300, 200), (5000, 1024, 1040)])
+def test_two_runs_give_the_same_bits(oracle_lib, t, n, k):
     g = gen(9)
-    t, n, k = 5000, 300, 200
     codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, torch.randn(t, k, generator=g, device=DEV)))
     dy = torch.randn(t, n, generator=g, device=DEV).to(torch.bfloat16)
     ws = workspace(t, n, k)
@@ -138,11 +142,14 @@ def test_two_runs_give_the_same_bits(oracle_lib):
     assert torch.equal(*runs)
 
 
-@pytest.mark.parametrize("dtype", TYPES)
-def test_offsets_past_32_bits(oracle_lib, dtype):
-    """dy with more than 2^32 elements: a stride that puts the last tokens far out."""
-    t, n, k = 40, 64, 64
-    stride = (1 << 32) // 36 // 8 * 8
+@pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 40, 64, 64), (torch.float32, 40, 64, 64),
+                                         (torch.bfloat16, 400, 1024, 1024), (torch.bfloat16, 257, 1024, 1024)])
+def test_offsets_past_32_bits(oracle_lib, dtype, t, n, k):
+    """dy with more than 2^32 elements: a stride that puts the last tokens far out
+    (in steps of less and of more than 2^25 elements)."""
+    stride = (1 << 32) // (t - 4) // 8 * 8
+    if t == 257:
+        stride = (1 << 25) + 8
     g = gen(3)
     small = torch.randint(-8, 9, (t, n), generator=g, device=DEV).to(dtype)
     big = torch.empty(t * stride, dtype=dtype, device=DEV)
