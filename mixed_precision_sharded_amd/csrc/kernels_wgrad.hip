@@ -88,17 +88,76 @@ __device__ __forceinline__ void store_dw(void* dw, int64_t i, float v, bool accu
     }
 }
 
+// Block b of `tiles` takes this tile: the device hands consecutive blocks to
+// its eight XCDs in turn, so each XCD (and its L2) gets a stretch of
+// neighbouring tiles, which share rows of dy.
+struct Tile {
+    int64_t n, k;
+};
+__device__ __forceinline__ Tile tile_of(uint32_t b, uint32_t tiles, uint32_t tiles_k)
+{
+    const uint32_t each = tiles / 8, more = tiles % 8, xcd = b % 8;
+    const uint32_t t = xcd * each + min(xcd, more) + b / 8;
+    return {static_cast<int64_t>(t / tiles_k), static_cast<int64_t>(t % tiles_k)};
+}
+
+// Where a block's tile goes: dw itself, or its split's partial sums.
+struct Target {
+    void* dw;
+    float* partials;  // or NULL
+    bool accumulate;
+    int64_t n_all, k_all;
+};
+
+// Stores a wavefront's kI x kJ results, whose first element is (n0, k0): lane
+// l of a result holds column l % 32 and the rows 8 (r / 4) + 4 (l / 32) + r % 4.
+template <bool kEdge, bool kBf16, bool kAccumulate, int kI, int kJ>
+__device__ __forceinline__ void store_results(const f32x16 (&acc)[kI][kJ], void* out, int64_t n0, int64_t k0, int64_t n_all,
+                                              int64_t k_all)
+{
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int64_t n = n0 + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const int64_t k = k0 + j * kFrag + lane % 32;
+                if (!kEdge || (n < n_all && k < k_all)) store_dw<kBf16>(out, n * k_all + k, acc[i][j][r], kAccumulate);
+            }
+        }
+    }
+}
+
+template <bool kDwBf16, int kI, int kJ>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[kI][kJ], const Target& to, int64_t n0, int64_t k0)
+{
+    const bool edge = n0 + kI * kFrag > to.n_all || k0 + kJ * kFrag > to.k_all;
+    if (to.partials) {
+        float* mine = to.partials + static_cast<int64_t>(blockIdx.y) * to.n_all * to.k_all;
+        if (edge) store_results<true, false, false>(acc, mine, n0, k0, to.n_all, to.k_all);
+        else store_results<false, false, false>(acc, mine, n0, k0, to.n_all, to.k_all);
+    } else if (to.accumulate) {
+        if (edge) store_results<true, kDwBf16, true>(acc, to.dw, n0, k0, to.n_all, to.k_all);
+        else store_results<false, kDwBf16, true>(acc, to.dw, n0, k0, to.n_all, to.k_all);
+    } else {
+        if (edge) store_results<true, kDwBf16, false>(acc, to.dw, n0, k0, to.n_all, to.k_all);
+        else store_results<false, kDwBf16, false>(acc, to.dw, n0, k0, to.n_all, to.k_all);
+    }
+}
+
 // One tile of dw over the t of [t_first, t_last): block (tile, split).
 template <bool kDyBf16, bool kDwBf16>
-__global__ __launch_bounds__(kBlock) void weight_grad_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
-                                                             int64_t k_all, int64_t per_split, uint32_t tiles_k,
-                                                             void* dw, bool accumulate, float* partials)
+__global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
+                                                                int64_t k_all, int64_t per_split, uint32_t tiles_k,
+                                                                Target to)
 {
     constexpr int kParts = kDyBf16 ? 1 : 3;
-    __shared__ __attribute__((aligned(16))) char tile_a[kParts][kTileT * kTile * 2];
-    __shared__ __attribute__((aligned(16))) char tile_b[kTileT * kTile * 2];
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x / tiles_k) * kTile;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x % tiles_k) * kTile;
+    constexpr int kBytes = kTileT * kTile * 2;
+    __shared__ __attribute__((aligned(16))) char lds[2][kParts + 1][kBytes];  // parts of dy, then x
+    const Tile tile = tile_of(blockIdx.x, gridDim.x, tiles_k);
+    const int64_t n0 = tile.n * kTile, k0 = tile.k * kTile;
     const int64_t padded = (k_all + kRun - 1) / kRun * kRun;
     const int64_t t_first = blockIdx.y * per_split;
     const int64_t t_last = min(t_first + per_split, tokens);
@@ -106,23 +165,37 @@ __global__ __launch_bounds__(kBlock) void weight_grad_kernel(Matrix dy, Codes x,
     const int wn = wave / 2 * 64, wk = wave % 2 * 64;
     f32x16 acc[2][2] = {};
 
-    for (int64_t t0 = t_first; t0 < t_last; t0 += kTileT) {
-        __syncthreads();
-        // 512 chunks of eight columns of each operand, two per thread.
+    // 512 chunks of eight columns of each operand, two per thread.
+    const int t_own = threadIdx.x / 16, chunk = threadIdx.x % 16;
+    const int64_t n = n0 + chunk * 8, k = k0 + chunk * 8;
+    Raw8<kDyBf16> raw[2];
+    u32x2 codes[2];
+    uint32_t byte[2];
+    auto load = [&](int64_t t0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int unit = threadIdx.x + j * kBlock;
-            const int t = unit / 16, chunk = unit % 16;
-            const bool live = t0 + t < t_last;
-            const int64_t n = n0 + chunk * 8;
-            const int64_t have = live ? n_all - n : 0;
-            const Raw8<kDyBf16> raw = load8<kDyBf16>(dy.data, (t0 + t) * dy.stride + n, have);
+            const int64_t t = t0 + t_own + j * 16;
+            const bool live = t < t_last;
+            raw[j] = load8<kDyBf16>(dy.data, t * dy.stride + n, live ? n_all - n : 0);
+            codes[j] = u32x2{0, 0};
+            byte[j] = 0;
+            if (live && k < padded) {
+                const int64_t u = (t * padded + k) / kUnit;
+                codes[j] = reinterpret_cast<const u32x2*>(x.codes)[u];
+                byte[j] = x.scales[u / 4];
+            }
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t at = chunk_at(t_own + j * 16, chunk);
             if (kDyBf16) {
-                *reinterpret_cast<u32x4*>(tile_a[0] + chunk_at(t, chunk)) = raw.v[0];
+                *reinterpret_cast<u32x4*>(lds[buf][0] + at) = raw[j].v[0];
             } else {
                 float v[kUnit];
                 uint32_t part[kUnit][3];
-                widen<kDyBf16>(raw, v);
+                widen<kDyBf16>(raw[j], v);
 #pragma unroll
                 for (int i = 0; i < kUnit; ++i) split3(v[i], part[i]);
 #pragma unroll
@@ -130,60 +203,46 @@ __global__ __launch_bounds__(kBlock) void weight_grad_kernel(Matrix dy, Codes x,
                     u32x4 w;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = part[2 * i][p] | part[2 * i + 1][p] << 16;
-                    *reinterpret_cast<u32x4*>(tile_a[p] + chunk_at(t, chunk)) = w;
+                    *reinterpret_cast<u32x4*>(lds[buf][p] + at) = w;
                 }
             }
-            const int64_t k = k0 + chunk * 8;
-            u32x2 codes{0, 0};
-            uint32_t byte = 0;
-            if (live && k < padded) {
-                const int64_t u = ((t0 + t) * padded + k) / kUnit;
-                codes = reinterpret_cast<const u32x2*>(x.codes)[u];
-                byte = x.scales[u / 4];
-            }
-            const float scale = __uint_as_float(byte << 23);
+            const float scale = __uint_as_float(byte[j] << 23);
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], scale, false));
-                w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], scale, true));
+                w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[j][i], scale, false));
+                w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[j][i], scale, true));
             }
-            *reinterpret_cast<u32x4*>(tile_b + chunk_at(t, chunk)) = w;
+            *reinterpret_cast<u32x4*>(lds[buf][kParts] + at) = w;
         }
-        __syncthreads();
+    };
+
+    load(t_first);
+    put(0);
+    load(t_first + kTileT);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t t0 = t_first; t0 < t_last; t0 += kTileT, buf ^= 1) {
 #pragma unroll
         for (int t = 0; t < kTileT; t += 16) {
             bf16x8 b[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) b[j] = read_operand(tile_b, t, wk + j * kFrag, lane);
+            for (int j = 0; j < 2; ++j) b[j] = read_operand(lds[buf][kParts], t, wk + j * kFrag, lane);
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const bf16x8 a = read_operand(tile_a[p], t, wn + i * kFrag, lane);
+                    const bf16x8 a = read_operand(lds[buf][p], t, wn + i * kFrag, lane);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
                 }
             }
         }
+        put(buf ^ 1);  // read last before the barrier that began this stage
+        load(t0 + 2 * kTileT);
+        __syncthreads();
     }
-    // Lane l of a result holds column l % 32 and the rows 8 (r / 4) + 4 (l / 32) + r % 4.
-    float* mine = partials ? partials + static_cast<int64_t>(blockIdx.y) * n_all * k_all : nullptr;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t k = k0 + wk + j * kFrag + lane % 32;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t n = n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4;
-                if (n < n_all && k < k_all) {
-                    if (mine) mine[n * k_all + k] = acc[i][j][r];
-                    else store_dw<kDwBf16>(dw, n * k_all + k, acc[i][j][r], accumulate);
-                }
-            }
-        }
-    }
+    store_tile<kDwBf16>(acc, to, n0 + wn, k0 + wk);
 }
 
 // ------------------------------------------------------------- wide tiles ---
@@ -202,7 +261,11 @@ __global__ __launch_bounds__(kBlock) void weight_grad_kernel(Matrix dy, Codes x,
 //
 // Rows behind the last token come as zeros of both operands (the buffer
 // resources end with the split's tokens); columns behind the matrix's own
-// read what lies there and are not stored.
+// read what lies there and are not stored.  Where dy's rows are not whole
+// 16-byte chunks (kAligned false: an odd width, stride or start) the last
+// chunk of a row reaches into the next row, which is harmless except in the
+// very last one: that token is left out of the stages and added to the sums
+// at the end, and the rows behind it are cleared in registers.
 
 constexpr int kWideTile = 256;
 constexpr int kWideT = 64;
@@ -214,10 +277,24 @@ __device__ __forceinline__ uint32_t wide_chunk_at(int t, int chunk)
     return static_cast<uint32_t>(t * kWideRow + ((chunk ^ ((t & 3) << 2)) << 4));
 }
 
-// Bytes from `from` to `to` that a buffer resource may reach.
-__device__ __forceinline__ uint32_t reach(int64_t bytes)
+// The order of a step's instructions: two LDS reads behind each of its first
+// eight matrix instructions and a write behind each of the next, with a load
+// from memory behind each of the first (asked for one by one, the compiler
+// gathers them before or behind the matrix instructions, which then wait:
+// 267 instead of 220 us for 8192 x 4096 x 4096; one read behind each of the
+// sixteen, with the writes last, took 238).
+template <int kWrites, int kLoads>
+__device__ __forceinline__ void order_step()
 {
-    return static_cast<uint32_t>(bytes < 0 ? 0 : (bytes > 0xfffffffcll ? 0xfffffffcll : bytes));
+    constexpr int kMfma = 0x008, kVmemRead = 0x020, kLdsRead = 0x100, kLdsWrite = 0x200;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        if (i < 8) __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
+        else if (i - 8 < kWrites) __builtin_amdgcn_sched_group_barrier(kLdsWrite, 1, 0);
+        if (i < kLoads) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 struct WideStage {
@@ -226,17 +303,18 @@ struct WideStage {
     uint32_t scale[4];
 };
 
-template <bool kDwBf16>
+template <bool kAligned, bool kDwBf16>
 __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
                                                                      int64_t k_all, int64_t per_split, uint32_t tiles_k,
-                                                                     void* dw, bool accumulate, float* partials)
+                                                                     Target to)
 {
     __shared__ __attribute__((aligned(16))) char lds[4 * kWideStage];  // dy: two stages, x: two stages
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x / tiles_k) * kWideTile;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x % tiles_k) * kWideTile;
+    const Tile tile = tile_of(blockIdx.x, gridDim.x, tiles_k);
+    const int64_t n0 = tile.n * kWideTile;
+    const int64_t k0 = tile.k * kWideTile;
     const int64_t padded = (k_all + kRun - 1) / kRun * kRun;
     const int64_t t_first = blockIdx.y * per_split;
-    const int64_t t_last = min(t_first + per_split, tokens);
+    const int64_t t_last = min(t_first + per_split, kAligned ? tokens : tokens - 1);
     const int stages = static_cast<int>((t_last - t_first + kWideT - 1) / kWideT);
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int wn = wave / 2 * 128, wk = wave % 2 * 128;
@@ -250,16 +328,29 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
     const uint8_t* x_base = x.codes + k0;
     const uint8_t* s_base = x.scales + k0 / kRun;
 
-    auto load_dy = [&](WideStage& w, int s, int first, int count) {
-        const int64_t t0 = t_first + static_cast<int64_t>(s) * kWideT;
-        const __amdgpu_buffer_rsrc_t r = rsrc(dy_base + t0 * dy_row, reach((t_last - t0) * dy_row - (dy.stride - n_all + n0) * 2));
+    // The operands' bytes behind a stage's first row, `row` for each of its tokens and `less` fewer in the last one; the
+    // stage behind the split's tokens, and those that follow, reach nothing.
+    const int t_count = static_cast<int>(t_last - t_first);
+    const int whole = t_count / kWideT, rest = t_count % kWideT;
+    const uint32_t dy_less = static_cast<uint32_t>((dy.stride - n_all + n0) * 2), x_less = static_cast<uint32_t>(k0);
+    auto reach = [&](int s, uint32_t row, uint32_t less) {
+        const uint32_t last = rest ? rest * row - less : 0u;
+        return s < whole ? kWideT * row - less : (s == whole ? last : 0u);
+    };
+    const char* dy_stage = dy_base + t_first * dy_row;
+    const uint8_t* x_stage = x_base + t_first * x_row;
+    const uint8_t* s_stage = s_base + t_first * (x_row / 32);
+    auto load_dy = [&](WideStage& w, int s, const char* at, int first, int count) {
+        // Not aligned: to the end of the matrix, which the last stages reach.
+        const int64_t left = kAligned ? 0 : (tokens - t_first - static_cast<int64_t>(s) * kWideT) * dy_row - dy_less;
+        const __amdgpu_buffer_rsrc_t r = rsrc(at, kAligned ? reach(s, dy_row, dy_less)
+                                                           : static_cast<uint32_t>(left < 0 ? 0 : min(left, 2ll * kWideT * dy_row)));
 #pragma unroll
         for (int j = first; j < first + count; ++j) w.dy[j] = load_u32x4<0>(r, dy_off + j * 8 * dy_row);
     };
-    auto load_x = [&](WideStage& w, int s, int first, int count) {
-        const int64_t t0 = t_first + static_cast<int64_t>(s) * kWideT;
-        const __amdgpu_buffer_rsrc_t r = rsrc(x_base + t0 * x_row, reach((t_last - t0) * x_row - k0));
-        const __amdgpu_buffer_rsrc_t rs = rsrc(s_base + t0 * (x_row / 32), reach((t_last - t0) * (x_row / 32) - k0 / kRun));
+    auto load_x = [&](WideStage& w, int s, const uint8_t* at, const uint8_t* scales_at, int first, int count) {
+        const __amdgpu_buffer_rsrc_t r = rsrc(at, reach(s, x_row, x_less));
+        const __amdgpu_buffer_rsrc_t rs = rsrc(scales_at, reach(s, x_row / 32, x_less / 32));
 #pragma unroll
         for (int j = first; j < first + count; ++j) {
             w.codes[j] = load_u32x4<0>(r, x_off + j * 16 * x_row);
@@ -267,27 +358,37 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
         }
     };
     const uint32_t dy_at = wide_chunk_at(tid / 32, tid % 32);              // + 8 rows: the same t & 3
-    const uint32_t x_at = 2 * kWideStage + wide_chunk_at(tid / 16, tid % 16 * 2);  // + 16 rows
-    auto put_dy = [&](const WideStage& w, int buf, int first, int count) {
+    // A unit fills two chunks.  Eight lanes write at a time; the last four of them take their second chunk first, so
+    // that the eight are spread over all banks (with every lane's first chunk first, each write took twice as long).
+    const bool swap = tid & 4;
+    const uint32_t x_at = 2 * kWideStage + wide_chunk_at(tid / 16, tid % 16 * 2) + (swap ? 16 : 0);  // + 16 rows
+    const uint32_t x_at2 = x_at ^ 16;
+    auto put_dy = [&](const WideStage& w, int s, int buf, int first, int count) {
 #pragma unroll
-        for (int j = first; j < first + count; ++j) *reinterpret_cast<u32x4*>(lds + buf * kWideStage + dy_at + j * 8 * kWideRow) = w.dy[j];
+        for (int j = first; j < first + count; ++j) {
+            u32x4 v = w.dy[j];
+            if (!kAligned) {
+                const uint32_t keep = s * kWideT + tid / 32 + j * 8 < t_count ? ~0u : 0u;
+                v = v & u32x4{keep, keep, keep, keep};
+            }
+            *reinterpret_cast<u32x4*>(lds + buf * kWideStage + dy_at + j * 8 * kWideRow) = v;
+        }
     };
     auto put_x = [&](const WideStage& w, int buf, int first, int count) {
 #pragma unroll
         for (int j = first; j < first + count; ++j) {
             const float scale = __uint_as_float(w.scale[j] << 23);
-            u32x4 lo, hi;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                lo[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][i], scale, false));
-                lo[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][i], scale, true));
-                hi[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][2 + i], scale, false));
-                hi[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.codes[j][2 + i], scale, true));
+            for (int h = 0; h < 2; ++h) {
+                const u32x2 c = swap == (h == 0) ? u32x2{w.codes[j][2], w.codes[j][3]} : u32x2{w.codes[j][0], w.codes[j][1]};
+                u32x4 v;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    v[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, false));
+                    v[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, true));
+                }
+                *reinterpret_cast<u32x4*>(lds + buf * kWideStage + (h == 0 ? x_at : x_at2) + j * 16 * kWideRow) = v;
             }
-            // A unit's two chunks differ in the lowest bit only, which the exclusive-or leaves.
-            char* p = lds + buf * kWideStage + x_at + j * 16 * kWideRow;
-            *reinterpret_cast<u32x4*>(p) = lo;
-            *reinterpret_cast<u32x4*>(p + 16) = hi;
         }
     };
     // Operand addresses: column block i of 32 sits at chunk 4 i, whose exclusive-or with the row is the lane's own.
@@ -324,57 +425,77 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
             for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
         }
     };
-    load_dy(w, 0, 0, 8);
-    load_x(w, 0, 0, 4);
-    put_dy(w, 0, 0, 8);
+    const int64_t dy_step = static_cast<int64_t>(kWideT) * dy_row, x_step = static_cast<int64_t>(kWideT) * x_row;
+    load_dy(w, 0, dy_stage, 0, 8);
+    load_x(w, 0, x_stage, s_stage, 0, 4);
+    put_dy(w, 0, 0, 0, 8);
     put_x(w, 0, 0, 4);
-    load_dy(w, 1, 0, 8);
-    load_x(w, 1, 0, 4);
+    // From here on the pointers are at the stage behind the one in work: its last two units of x are still to come.
+    dy_stage += dy_step, x_stage += x_step, s_stage += x_step / 32;
+    load_dy(w, 1, dy_stage, 0, 8);
+    load_x(w, 1, x_stage, s_stage, 0, 2);
     __syncthreads();
     read4(a[0], a_at, 0, 0);
     read4(b[0], b_at, 0, 0);
-    for (int s = 0; s < stages; ++s) {
-        const int buf = s & 1;
+    __builtin_amdgcn_sched_barrier(0);
+    auto stage = [&](int s, int buf) {
         read4(a[1], a_at, buf, 1);
         read4(b[1], b_at, buf, 1);
-        put_dy(w, buf ^ 1, 0, 4);
-        put_x(w, buf ^ 1, 0, 1);
-        load_dy(w, s + 2, 0, 4);
-        load_x(w, s + 2, 0, 1);
+        load_x(w, s + 1, x_stage, s_stage, 2, 2);
         multiply(0);
+        put_dy(w, s + 1, buf ^ 1, 0, 4);
+        put_x(w, buf ^ 1, 0, 1);
+        dy_stage += dy_step, x_stage += x_step, s_stage += x_step / 32;
+        order_step<6, 4>();
         read4(a[0], a_at, buf, 2);
         read4(b[0], b_at, buf, 2);
-        put_dy(w, buf ^ 1, 4, 4);
-        put_x(w, buf ^ 1, 1, 1);
-        load_dy(w, s + 2, 4, 4);
-        load_x(w, s + 2, 1, 1);
+        load_dy(w, s + 2, dy_stage, 0, 4);
+        load_x(w, s + 2, x_stage, s_stage, 0, 1);
         multiply(1);
+        put_dy(w, s + 1, buf ^ 1, 4, 4);
+        put_x(w, buf ^ 1, 1, 1);
+        order_step<6, 6>();
         read4(a[1], a_at, buf, 3);
         read4(b[1], b_at, buf, 3);
-        put_x(w, buf ^ 1, 2, 2);
-        load_x(w, s + 2, 2, 2);
+        load_dy(w, s + 2, dy_stage, 4, 4);
+        load_x(w, s + 2, x_stage, s_stage, 1, 1);
         multiply(0);
+        put_x(w, buf ^ 1, 2, 2);
+        order_step<4, 6>();
         __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
         read4(a[0], a_at, buf ^ 1, 0);
         read4(b[0], b_at, buf ^ 1, 0);
         multiply(1);
+        order_step<0, 0>();
+    };
+    // Two stages a round, so that the buffers' addresses are constants of the code (4 % faster).
+    int s = 0;
+    for (; s + 1 < stages; s += 2) {
+        stage(s, 0);
+        stage(s + 1, 1);
     }
-    float* mine = partials ? partials + static_cast<int64_t>(blockIdx.y) * n_all * k_all : nullptr;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    if (s < stages) stage(s, 0);
+    if (!kAligned && t_first + per_split >= tokens) {
+        const int64_t t = tokens - 1;
+        float xv[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t k = k0 + wk + j * kFrag + lane % 32;
+            const int64_t k = min(k0 + wk + j * kFrag + lane % 32, padded - 1);
+            xv[j] = decode1<true>(x.codes[t * padded + k], scale_value(x.scales[t * (padded / kRun) + k / kRun]));
+        }
+        const uint16_t* last = static_cast<const uint16_t*>(dy.data) + t * dy.stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int64_t n = n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4;
-                if (n < n_all && k < k_all) {
-                    if (mine) mine[n * k_all + k] = acc[i][j][r];
-                    else store_dw<kDwBf16>(dw, n * k_all + k, acc[i][j][r], accumulate);
-                }
+                const float d = bf16_lo(last[min(n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4, n_all - 1)]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j][r] = __builtin_fmaf(d, xv[j], acc[i][j][r]);
             }
         }
     }
+    store_tile<kDwBf16>(acc, to, n0 + wn, k0 + wk);
 }
 
 // dw = [dw +] the splits' partial sums, in split order.
@@ -425,14 +546,19 @@ Shape shape_of(int64_t tokens, int64_t n, int64_t k, int tile, int stage_t, int 
 }
 
 Shape narrow_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kTile, kTileT, 2, 1.2); }
-Shape wide_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kWideTile, kWideT, 1, 2.0); }
+Shape wide_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kWideTile, kWideT, 1, 1.6); }
 
-// The wide tile takes bf16 gradients whose rows are whole 16-byte chunks.
+// Whether dy's rows are whole 16-byte chunks.
+bool chunk_rows(const Matrix& dy, int64_t n)
+{
+    return n % 8 == 0 && dy.stride % 8 == 0 && reinterpret_cast<uintptr_t>(dy.data) % 16 == 0;
+}
+
+// The wide tile takes bf16 gradients of rows that keep two stages' offsets
+// below 2^32 bytes.
 bool wide_fits(const Matrix& dy, bool dy_bf16, int64_t tokens, int64_t n, int64_t k)
 {
-    if (!dy_bf16 || n % 8 || dy.stride % 8 || reinterpret_cast<uintptr_t>(dy.data) % 16) return false;
-    if (dy.stride >= 1 << 25) return false;  // a stage's offsets stay below 2^32 bytes
-    return tokens >= 256 && n * k >= 1 << 20;
+    return dy_bf16 && dy.stride < 1 << 23 && k <= 1 << 25 && tokens >= 256 && n * k >= 1 << 20;
 }
 
 size_t scratch_of(const Shape& s, int64_t n, int64_t k)
@@ -460,12 +586,15 @@ hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tok
     const dim3 grid(static_cast<uint32_t>(s.tiles_n * s.tiles_k), s.splits);
     const uint32_t tk = static_cast<uint32_t>(s.tiles_k);
     auto run = [&](auto kernel) {
-        kernel<<<grid, kBlock, 0, stream>>>(dy, x, tokens, out_features, in_features, s.per_split, tk, dw, accumulate,
-                                            partials);
+        kernel<<<grid, kBlock, 0, stream>>>(dy, x, tokens, out_features, in_features, s.per_split, tk,
+                                            Target{dw, partials, accumulate, out_features, in_features});
     };
-    if (wide) {
-        if (dw_bf16) run(weight_grad_wide_kernel<true>);
-        else run(weight_grad_wide_kernel<false>);
+    if (wide && chunk_rows(dy, out_features)) {
+        if (dw_bf16) run(weight_grad_wide_kernel<true, true>);
+        else run(weight_grad_wide_kernel<true, false>);
+    } else if (wide) {
+        if (dw_bf16) run(weight_grad_wide_kernel<false, true>);
+        else run(weight_grad_wide_kernel<false, false>);
     } else if (dy_bf16) {
         if (dw_bf16) run(weight_grad_kernel<true, true>);
         else run(weight_grad_kernel<true, false>);
