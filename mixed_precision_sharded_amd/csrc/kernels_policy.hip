@@ -11,6 +11,12 @@
 namespace mps {
 namespace {
 
+// Cache policy of the gradient's stores (2: nontemporal).  The rows in work
+// stay in the cache and the gradient passes it by: 8192 x 128256 bf16 811 ->
+// 795 us, 1000 x 50257 58 -> 41 us.  The logits' loads keep the default
+// (nontemporal, 5-40 % slower: the second reading then misses).
+constexpr int kGradientPolicy = 2;
+constexpr int kLogitsPolicy = 0;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // 2^((x - top) log2(e)), the form that also holds at the type's lowest values
@@ -32,47 +38,61 @@ __device__ __forceinline__ Share join(const Share& a, const Share& b)
     return {top, a.sum * static_cast<double>(exp_below(a.top, base)) + b.sum * static_cast<double>(exp_below(b.top, base))};
 }
 
-// One value a row: what the row gives to the loss, and the two factors of
-// its gradient, dlogits = slope * onehot + factor * e^(x - top).
+// What one row gives to the loss, and the two factors of its gradient,
+// dlogits = slope * onehot + factor * e^(x - top).
 struct RowResult {
     double loss;
-    float logp, kl, slope, factor, top;
+    float logp, kl, slope, factor, top, label_logit;
 };
 
-// `share` is the whole row's; `label_logit` its label's.  A row that is left
-// out never comes here.
-__device__ __forceinline__ RowResult row_result(const PolicyArgs& a, int64_t row, const Share& share, float label_logit)
+// The fp64 part of a row, for the lanes that own one.  Not inlined: its
+// registers would count for the streaming loops, which want many wavefronts.
+__device__ __attribute__((noinline)) RowResult row_values(float top, double sum, float label_logit, bool loss_too, bool with_ref,
+                                                          float old_logp, float ref_logp, float advantage, float weight,
+                                                          double low, double high, double kl_coef)
 {
     RowResult r = {};
-    if (share.top == -INFINITY && share.sum == 0.0) return r;  // nothing to choose from: left out
-    r.top = share.top;
-    const double logp = static_cast<double>(label_logit) - static_cast<double>(share.top) - log(share.sum);
+    if (top == -INFINITY && sum == 0.0) return r;  // nothing to choose from: left out
+    r.top = top;
+    r.label_logit = label_logit;
+    const double logp = static_cast<double>(label_logit) - static_cast<double>(top) - log(sum);
     r.logp = static_cast<float>(logp);
-    if (!a.loss) return r;
-    const double w = a.weight[row], adv = a.advantage[row];
+    if (!loss_too) return r;
+    const double w = weight, adv = advantage;
     double gain = 0.0, slope = 0.0;
     if (adv != 0.0) {
-        const double ratio = exp(logp - static_cast<double>(a.old_logp[row]));
-        const double low = 1.0 - a.clip_low, high = 1.0 + a.clip_high;
+        const double ratio = exp(logp - static_cast<double>(old_logp));
         const double held = ratio < low ? low : (ratio > high ? high : ratio);  // a NaN stays one
         const double plain = ratio * adv, clipped = held * adv;
         const bool flat = plain > clipped;
         gain = flat ? clipped : plain;
         slope = flat ? 0.0 : -plain;
     }
-    if (a.ref_logp) {
-        const double d = static_cast<double>(a.ref_logp[row]) - logp;
+    if (with_ref) {
+        const double d = static_cast<double>(ref_logp) - logp;
         const double q = exp(d);
         const double kl = q == INFINITY ? q : q - d - 1.0;  // the label has no probability left
         r.kl = static_cast<float>(kl);
-        gain -= a.kl_coef * kl;
-        slope += a.kl_coef * (1.0 - q);
+        gain -= kl_coef * kl;
+        slope += kl_coef * (1.0 - q);
     }
     r.loss = -w * gain;
     slope *= w;
     r.slope = static_cast<float>(slope);
-    r.factor = static_cast<float>(-slope / share.sum);
+    r.factor = static_cast<float>(-slope / sum);
     return r;
+}
+
+__device__ __forceinline__ float logit_at(const PolicyArgs& a, bool bf16, int64_t i)
+{
+    if (bf16) return bf16_lo(static_cast<const uint16_t*>(a.logits.data)[i]);
+    return static_cast<const float*>(a.logits.data)[i];
+}
+
+__device__ __forceinline__ void store_logit(const PolicyArgs& a, bool bf16, int64_t i, float v)
+{
+    if (bf16) static_cast<uint16_t*>(a.dlogits.data)[i] = bf16_one(v);
+    else static_cast<float*>(a.dlogits.data)[i] = v;
 }
 
 // Whether a row takes part at all.
@@ -82,32 +102,360 @@ __device__ __forceinline__ bool row_live(const PolicyArgs& a, int64_t row)
     return label >= 0 && label < a.vocab && !(a.weight && a.weight[row] == 0.0f);
 }
 
-// The block's shares joined in a fixed order; every thread gets the result.
-__device__ __forceinline__ Share block_join(Share s, Share* lds)
+// The result of a live row whose share this is, and its own outputs; one lane
+// per row.
+__device__ __forceinline__ RowResult finish_row(const PolicyArgs& a, bool bf16, int64_t row, bool live, const Share& s)
 {
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const Share o = {__shfl_xor(s.top, off, kWave), __shfl_xor(s.sum, off, kWave)};
-        s = (threadIdx.x & off) ? join(o, s) : join(s, o);
+    RowResult r = {};
+    if (live) {
+        const bool loss_too = a.loss != nullptr, with_ref = a.ref_logp != nullptr;
+        r = row_values(s.top, s.sum, logit_at(a, bf16, row * a.logits.stride + a.labels[row]), loss_too, with_ref,
+                       loss_too ? a.old_logp[row] : 0.0f, with_ref ? a.ref_logp[row] : 0.0f, loss_too ? a.advantage[row] : 0.0f,
+                       loss_too ? a.weight[row] : 0.0f, 1.0 - a.clip_low, 1.0 + a.clip_high, a.kl_coef);
     }
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
-    __syncthreads();
-    Share r = lds[0];
-    for (int w = 1; w < static_cast<int>(blockDim.x) / kWave; ++w) r = join(r, lds[w]);
+    if (a.token_logp) a.token_logp[row] = r.logp;
+    if (a.token_kl) a.token_kl[row] = r.kl;
     return r;
 }
 
-// Units of eight logits of one share of a row: [first, last).
+// Joins the shares of the first `n` (a power of two) lanes of each group of
+// n, in a fixed order; every lane of the group gets the result.
+template <int kLanes>
+__device__ __forceinline__ Share lanes_join(Share s)
+{
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) {
+        const Share o = {__shfl_xor(s.top, off, kWave), __shfl_xor(s.sum, off, kWave)};
+        s = (lane & off) ? join(o, s) : join(s, o);
+    }
+    return s;
+}
+
+constexpr int kDeep = 4;  // units of eight logits that a thread has under way
+
+// A thread's running largest logit, and the sum under it.
+struct Running {
+    float top = -INFINITY, sum = 0.0f;
+
+    template <bool kBf16>
+    __device__ __forceinline__ void take(const Raw8<kBf16>& raw)
+    {
+        float x[kUnit];
+        widen<kBf16>(raw, x);
+        const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        const float now = fmaxf(top, most), under = now == -INFINITY ? 0.0f : now;
+        const float before = sum * exp_below(top, under);
+        top = now;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) x[i] = exp_below(x[i], under);
+        sum = before + (((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+    }
+};
+
+// The whole units of (a stretch of) a row, through a buffer resource: one
+// 32-bit offset per thread and a constant per access, where pointers would
+// take two registers each.  A unit behind the last one reads as zeros and is
+// not stored.
+template <bool kBf16>
+struct Units {
+    static constexpr uint32_t kBytes = kUnit * (kBf16 ? 2 : 4);
+    __amdgpu_buffer_rsrc_t r;
+
+    __device__ __forceinline__ Units(const void* data, int64_t at, uint32_t units)
+        : r(rsrc(uniform_ptr(static_cast<const char*>(data) + at * (kBf16 ? 2 : 4)), units * kBytes))
+    {
+    }
+
+    // Unit `unit` + `more`, the second the same in every lane.
+    __device__ __forceinline__ Raw8<kBf16> load(uint32_t unit, uint32_t more) const
+    {
+        Raw8<kBf16> v;
+        v.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes, more * kBytes, kLogitsPolicy);
+        if (!kBf16) v.v[kBf16 ? 0 : 1] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes + 16, more * kBytes, kLogitsPolicy);
+        return v;
+    }
+
+    __device__ __forceinline__ void store(const float (&x)[kUnit], uint32_t unit, uint32_t more) const
+    {
+        if (kBf16) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16_pack2(x[2 * i], x[2 * i + 1]);
+            __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes, more * kBytes, kGradientPolicy);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 w = {__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), __float_as_uint(x[4 * h + 2]),
+                                 __float_as_uint(x[4 * h + 3])};
+                __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes + 16 * h, more * kBytes, kGradientPolicy);
+            }
+        }
+    }
+
+    // Stores factor * e^(x - top) of a unit.
+    __device__ __forceinline__ void give(const Raw8<kBf16>& raw, float factor, float top, uint32_t unit, uint32_t more) const
+    {
+        float x[kUnit];
+        widen<kBf16>(raw, x);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) x[i] = factor * exp_below(x[i], top);
+        store(x, unit, more);
+    }
+};
+
+// Forgets, for the compiler, what is known of these registers.  Without it
+// the widened values of one pass over a kept row are held for the next, twice
+// the row's size in registers that are not there.
+template <bool kBf16>
+__device__ __forceinline__ void forget(Raw8<kBf16>& r)
+{
+#pragma unroll
+    for (int i = 0; i < (kBf16 ? 1 : 2); ++i) asm volatile("" : "+v"(r.v[i]));
+}
+
+// The share of thread `t` of kTeam in the logits [first, last) of a row, both
+// in whole units except that `last` may be the row's end.
+template <bool kBf16, int kTeam>
+__device__ __forceinline__ Share read_share(const PolicyArgs& a, int64_t row, int64_t first, int64_t last, int t)
+{
+    const uint32_t count = static_cast<uint32_t>(last - first), full = count / kUnit;
+    const Units<kBf16> in(a.logits.data, row * a.logits.stride + first, full);
+    Running run;
+    uint32_t u = t;
+    for (; u + (kDeep - 1) * kTeam < full; u += kDeep * kTeam) {
+        Raw8<kBf16> raw[kDeep];
+#pragma unroll
+        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u, v * kTeam);
+#pragma unroll
+        for (int v = 0; v < kDeep; ++v) run.take(raw[v]);
+    }
+    for (; u < full; u += kTeam) run.take(in.load(u, 0));
+    Share s = {run.top, static_cast<double>(run.sum)};
+    if (t < static_cast<int>(count % kUnit)) {
+        const float x = logit_at(a, kBf16, row * a.logits.stride + first + full * kUnit + t);
+        s = join(s, {x, x == -INFINITY ? 0.0 : static_cast<double>(exp_below(x, x))});
+    }
+    return s;
+}
+
+// The gradient of the logits [first, last) of a row, by thread t of kTeam;
+// the thread that has stored the label's element stores it once more with the
+// slope added.
+template <bool kBf16, int kTeam>
+__device__ __forceinline__ void write_gradient(const PolicyArgs& a, int64_t row, int64_t first, int64_t last, int t,
+                                               const RowResult& r, int64_t label)
+{
+    const int64_t to = row * a.dlogits.stride + first;
+    const uint32_t count = static_cast<uint32_t>(last - first), full = count / kUnit;
+    const Units<kBf16> out(a.dlogits.data, to, full);
+    const float top = r.top, factor = r.factor;
+    uint32_t u = t;
+    if (r.slope == 0.0f && factor == 0.0f) {  // zeros, whatever the logits
+        const float x[kUnit] = {};
+        for (; u < full; u += kTeam) out.store(x, u, 0);
+        if (t < static_cast<int>(count % kUnit)) store_logit(a, kBf16, to + full * kUnit + t, 0.0f);
+        return;
+    }
+    const Units<kBf16> in(a.logits.data, row * a.logits.stride + first, full);
+    for (; u + (kDeep - 1) * kTeam < full; u += kDeep * kTeam) {
+        Raw8<kBf16> raw[kDeep];
+#pragma unroll
+        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u, v * kTeam);
+#pragma unroll
+        for (int v = 0; v < kDeep; ++v) out.give(raw[v], factor, top, u, v * kTeam);
+    }
+    for (; u < full; u += kTeam) out.give(in.load(u, 0), factor, top, u, 0);
+    if (t < static_cast<int>(count % kUnit)) {
+        const int64_t c = full * kUnit + t;
+        store_logit(a, kBf16, to + c, factor * exp_below(logit_at(a, kBf16, row * a.logits.stride + first + c), top));
+    }
+    if (label < first || label >= last) return;
+    const uint32_t at = static_cast<uint32_t>(label - first);
+    const uint32_t owner = at / kUnit < full ? at / kUnit % kTeam : at % kUnit;
+    if (owner == static_cast<uint32_t>(t)) store_logit(a, kBf16, to + at, factor * exp_below(r.label_logit, top) + r.slope);
+}
+
+// ------------------------------------------------------ a row per block ---
+
+// The shares of a block's wavefronts, joined and finished by the first one;
+// the result is in `result` behind the barrier.  Called by every thread.
+template <bool kBf16, int kThreads>
+__device__ __forceinline__ void finish_block(const PolicyArgs& a, int64_t row, bool live, Share mine, Share* shares,
+                                             RowResult* result, double& total)
+{
+    constexpr int kWaves = kThreads / kWave;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    if (live) {
+        mine = lanes_join<kWave>(mine);
+        if (lane == 0) shares[wave] = mine;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const Share s = lanes_join<kWaves>(shares[lane % kWaves]);
+        if (lane == 0) {
+            *result = finish_row(a, kBf16, row, live, s);
+            total += result->loss;
+        }
+    }
+    __syncthreads();
+}
+
+// Block b takes rows b, b + grid, ..; the sum of their losses goes to
+// losses[b].  The rows are read twice.
+template <bool kBf16>
+__global__ __launch_bounds__(kBlock) void policy_block_kernel(PolicyArgs a, double* losses)
+{
+    __shared__ Share shares[kWavesPerBlock];
+    __shared__ RowResult result;
+    double total = 0.0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const bool live = row_live(a, row);
+        Share s = {-INFINITY, 0.0};
+        if (live) s = read_share<kBf16, kBlock>(a, row, 0, a.vocab, threadIdx.x);
+        finish_block<kBf16, kBlock>(a, row, live, s, shares, &result, total);
+        if (a.dlogits.data) write_gradient<kBf16, kBlock>(a, row, 0, a.vocab, threadIdx.x, result, a.labels[row]);
+    }
+    if (threadIdx.x == 0 && losses) losses[blockIdx.x] = total;
+}
+
+// The same for long rows, which are kept between the passes: unit t + j *
+// kThreads of thread t in registers for j < kRegs, in LDS (each thread's own
+// place, so that no barrier is needed) for the next kLds, and only what lies
+// behind is read again.  A register that has given its gradient asks for the
+// next row's unit at once, so half of the next row is on its way while this
+// one is written.  Rows of at least kThreads * kRegs units of eight.
+template <bool kBf16, int kThreads, int kRegs, int kLds>
+__global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, double* losses)
+{
+    constexpr int kWords = kBf16 ? 1 : 2, kHalf = kLds / 2;
+    __shared__ u32x4 kept[kLds * kWords * kThreads];
+    __shared__ Share shares[kThreads / kWave];
+    __shared__ RowResult result;
+    const uint32_t t = threadIdx.x, full = static_cast<uint32_t>(a.vocab / kUnit), rest = static_cast<uint32_t>(a.vocab % kUnit);
+    double total = 0.0;
+    Raw8<kBf16> reg[kRegs];
+    auto load_regs = [&](const Units<kBf16>& in) {
+#pragma unroll
+        for (int j = 0; j < kRegs; ++j) reg[j] = in.load(t, j * kThreads);
+    };
+    int64_t row = blockIdx.x;
+    bool live = row < a.rows && row_live(a, row);
+    if (live) load_regs(Units<kBf16>(a.logits.data, row * a.logits.stride, full));
+    while (row < a.rows) {
+        const Units<kBf16> in(a.logits.data, row * a.logits.stride, full);
+        Share s = {-INFINITY, 0.0};
+        if (live) {
+            Running run;
+            Raw8<kBf16> raw[kHalf];
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) raw[j] = in.load(t, (kRegs + j) * kThreads);
+#pragma unroll
+            for (int j = 0; j < kRegs; ++j) run.take(reg[j]);  // whole: the row has as many units
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) {
+                    const int at = h * kHalf + j;
+                    for (int w = 0; w < kWords; ++w) kept[(at * kWords + w) * kThreads + t] = raw[j].v[w];
+                    if (t + (kRegs + at) * kThreads < full) run.take(raw[j]);
+                    if (h == 0) raw[j] = in.load(t, (kRegs + kHalf + j) * kThreads);
+                }
+            }
+            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) run.take(in.load(u, 0));
+            s = {run.top, static_cast<double>(run.sum)};
+            if (t < rest) {
+                const float x = logit_at(a, kBf16, row * a.logits.stride + full * kUnit + t);
+                s = join(s, {x, x == -INFINITY ? 0.0 : static_cast<double>(exp_below(x, x))});
+            }
+        }
+        finish_block<kBf16, kThreads>(a, row, live, s, shares, &result, total);
+        const int64_t next = row + gridDim.x;
+        const bool next_live = next < a.rows && row_live(a, next);
+        const Units<kBf16> coming(a.logits.data, next * a.logits.stride, full);
+        const float top = result.top, factor = result.factor, slope = result.slope;
+        if (!a.dlogits.data || (slope == 0.0f && factor == 0.0f)) {  // no gradient, or zeros whatever the logits
+            if (next_live) load_regs(coming);
+            if (a.dlogits.data) write_gradient<kBf16, kThreads>(a, row, 0, a.vocab, t, result, -1);
+        } else {
+            const int64_t to = row * a.dlogits.stride;
+            const Units<kBf16> out(a.dlogits.data, to, full);
+#pragma unroll
+            for (int j = 0; j < kRegs; ++j) {
+                forget(reg[j]);
+                out.give(reg[j], factor, top, t, j * kThreads);
+                if (next_live) reg[j] = coming.load(t, j * kThreads);
+            }
+#pragma unroll
+            for (int j = 0; j < kLds; ++j) {
+                Raw8<kBf16> raw;
+                for (int w = 0; w < kWords; ++w) raw.v[w] = kept[(j * kWords + w) * kThreads + t];
+                out.give(raw, factor, top, t, (kRegs + j) * kThreads);
+            }
+            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) out.give(in.load(u, 0), factor, top, u, 0);
+            if (t < rest) {
+                const int64_t c = full * kUnit + t;
+                store_logit(a, kBf16, to + c, factor * exp_below(logit_at(a, kBf16, row * a.logits.stride + c), top));
+            }
+            const uint32_t label = static_cast<uint32_t>(a.labels[row]);
+            const uint32_t owner = label / kUnit < full ? label / kUnit % kThreads : label % kUnit;
+            if (owner == t) store_logit(a, kBf16, to + label, factor * exp_below(result.label_logit, top) + slope);
+        }
+        row = next;
+        live = next_live;
+    }
+    if (threadIdx.x == 0 && losses) losses[blockIdx.x] = total;
+}
+
+// -------------------------------------------------- a row per wavefront ---
+
+// For short rows: a block takes kGroup rows at a time, a wavefront one of
+// them after the other, and the rows' fp64 parts run side by side on kGroup
+// lanes.
+constexpr int kGroup = 16;
+
+template <bool kBf16>
+__global__ __launch_bounds__(kBlock) void policy_wave_kernel(PolicyArgs a, double* losses)
+{
+    __shared__ Share shares[kGroup];
+    __shared__ RowResult results[kGroup];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    double total = 0.0;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroup; first < a.rows; first += static_cast<int64_t>(gridDim.x) * kGroup) {
+        const int n = static_cast<int>(min(static_cast<int64_t>(kGroup), a.rows - first));
+        for (int i = wave; i < n; i += kWavesPerBlock) {
+            if (!row_live(a, first + i)) continue;
+            const Share s = lanes_join<kWave>(read_share<kBf16, kWave>(a, first + i, 0, a.vocab, lane));
+            if (lane == 0) shares[i] = s;
+        }
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < n) {
+            const int64_t row = first + threadIdx.x;
+            results[threadIdx.x] = finish_row(a, kBf16, row, row_live(a, row), shares[threadIdx.x]);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < n; ++i) total += results[i].loss;
+        }
+        if (!a.dlogits.data) continue;
+        for (int i = wave; i < n; i += kWavesPerBlock) {
+            write_gradient<kBf16, kWave>(a, first + i, 0, a.vocab, lane, results[i], a.labels[first + i]);
+        }
+    }
+    if (threadIdx.x == 0 && losses) losses[blockIdx.x] = total;
+}
+
+// -------------------------------------------------- several blocks a row ---
+
+// Logits of one share of a row.
 struct Span {
     int64_t first, last;
 };
 __device__ __forceinline__ Span span_of(int64_t vocab, int shares, int share)
 {
     const int64_t units = (vocab + kUnit - 1) / kUnit;
-    const int64_t per = (units + shares - 1) / shares;
-    const int64_t first = per * share;
-    return {first, first + per < units ? first + per : units};
+    const int64_t per = (units + shares - 1) / shares * kUnit;
+    return {min(per * share, vocab), min(per * (share + 1), vocab)};
 }
 
 // Shares of every row: block (row, share).
@@ -118,64 +466,40 @@ __global__ __launch_bounds__(kBlock) void policy_shares_kernel(PolicyArgs a, int
     const Span span = span_of(a.vocab, shares, blockIdx.y);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         if (!row_live(a, row)) continue;
-        Share s = {-INFINITY, 0.0};
-        for (int64_t u = span.first + threadIdx.x; u < span.last; u += kBlock) {
-            float x[kUnit], top = -INFINITY, sum = 0.0f;
-            const int64_t c = u * kUnit, n = a.vocab - c;
-            widen<kBf16>(load8<kBf16>(a.logits.data, row * a.logits.stride + c, n), x);
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) {
-                x[i] = i < n ? x[i] : -INFINITY;
-                top = fmaxf(top, x[i]);
-            }
-            top = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) sum += exp_below(x[i], top);
-            s = join(s, {sum == 0.0f ? -INFINITY : top, static_cast<double>(sum)});
+        Share s = lanes_join<kWave>(read_share<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x));
+        __syncthreads();
+        if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
+        __syncthreads();
+        if (threadIdx.x < kWave) {
+            s = lanes_join<kWavesPerBlock>(lds[threadIdx.x % kWavesPerBlock]);
+            if (threadIdx.x == 0) out[row * shares + blockIdx.y] = s;
         }
-        s = block_join(s, lds);
-        if (threadIdx.x == 0) out[row * shares + blockIdx.y] = s;
     }
 }
 
-// Joins the shares of a row, and writes this block's part of the gradient;
-// the first share's block writes the row's own results.
+// Joins the (at most 64) shares of a row, and writes this block's part of the
+// gradient; the first share's block writes the row's own results.
 template <bool kBf16>
-__global__ __launch_bounds__(kBlock) void policy_rows_kernel(PolicyArgs a, int shares, const Share* in, double* row_loss)
+__global__ __launch_bounds__(kBlock) void policy_rows_kernel(PolicyArgs a, int shares, const Share* in, double* losses)
 {
+    __shared__ RowResult result;
     const Span span = span_of(a.vocab, shares, blockIdx.y);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        RowResult r = {};
-        int64_t label = -1;
-        if (row_live(a, row)) {
-            label = a.labels[row];
-            float x;
-            if (kBf16) x = bf16_lo(static_cast<const uint16_t*>(a.logits.data)[row * a.logits.stride + label]);
-            else x = static_cast<const float*>(a.logits.data)[row * a.logits.stride + label];
-            Share s = in[row * shares];
-            for (int i = 1; i < shares; ++i) s = join(s, in[row * shares + i]);
-            r = row_result(a, row, s, x);
-        }
-        if (blockIdx.y == 0 && threadIdx.x == 0) {
-            if (a.token_logp) a.token_logp[row] = r.logp;
-            if (a.token_kl) a.token_kl[row] = r.kl;
-            if (row_loss) row_loss[row] = r.loss;
-        }
-        if (!a.dlogits.data) continue;
-        const bool flat = r.slope == 0.0f && r.factor == 0.0f;  // zeros, whatever the logits
-        for (int64_t u = span.first + threadIdx.x; u < span.last; u += kBlock) {
-            float x[kUnit] = {};
-            const int64_t c = u * kUnit, n = a.vocab - c;
-            if (!flat) {
-                widen<kBf16>(load8<kBf16>(a.logits.data, row * a.logits.stride + c, n), x);
-#pragma unroll
-                for (int i = 0; i < kUnit; ++i) {
-                    x[i] = r.factor * exp_below(x[i], r.top);
-                    if (c + i == label) x[i] += r.slope;
-                }
+        __syncthreads();
+        if (threadIdx.x < kWave) {
+            const bool live = row_live(a, row);
+            const int lane = threadIdx.x;
+            const Share s = lanes_join<kWave>(live && lane < shares ? in[row * shares + lane] : Share{-INFINITY, 0.0});
+            if (lane == 0) {
+                // Every block computes the row's values; the first one's are kept.
+                PolicyArgs mine = a;
+                if (blockIdx.y != 0) mine.token_logp = mine.token_kl = nullptr;
+                result = finish_row(mine, kBf16, row, live, s);
+                if (blockIdx.y == 0 && losses) losses[row] = result.loss;
             }
-            store8<kBf16>(x, a.dlogits.data, row * a.dlogits.stride + c, n);
         }
+        __syncthreads();
+        if (a.dlogits.data) write_gradient<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x, result, a.labels[row]);
     }
 }
 
@@ -189,15 +513,32 @@ __global__ __launch_bounds__(kBlock) void policy_total_kernel(const double* valu
     if (threadIdx.x == 0) *loss = static_cast<float>(s);
 }
 
-constexpr int kMostRowBlocks = 1 << 20;
+// Which kernel takes a call, by rows and vocabulary (measured with all of
+// them forced on the same calls, us):
+//   - up to kWaveVocab logits a row is a wavefront's: 8000 x 5000 bf16 45
+//     against 67 with a block each, 30000 x 1000 45 against 109;
+//   - above, a block's of 256 threads that reads it twice, up to kBlockVocab
+//     logits: 2000 x 9000 bf16 22.5 against 28 kept, 1000 x 12000 fp32 24
+//     against 25;
+//   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 30 against
+//     34, 8192 x 128256 bf16 811 against 1200, 2000 x 65000 fp32 231 against
+//     315; 1000 x 32003 fp32 58 against 75;
+//   - up to kFewRows rows, blocks share a row: 24 x 128256 bf16 19 against 22.
+constexpr int64_t kWaveVocab = 8192;
+constexpr int64_t kBlockVocab = 16384;
+constexpr int64_t kFewRows = 64;
+constexpr int kShareUnits = 1024;  // units of eight logits in a share, at least
+constexpr int kMostShares = kWave;
+constexpr int kMostBlocks = 2048;
 
-// Blocks that share a row: enough for two blocks per CU, of at least 16
-// units per thread each.
+// Blocks that share a row, where rows are few and long: two blocks per CU in
+// all.  1: a row per block or per wavefront.
 int shares_of(int64_t rows, int64_t vocab)
 {
-    const int64_t most = (vocab + kUnit * kBlock * 4 - 1) / (kUnit * kBlock * 4);
-    int64_t s = 1024 / (rows > 0 ? rows : 1);
-    if (s > most) s = most;
+    if (rows <= 0 || rows > kFewRows) return 1;
+    int64_t s = vocab / (kShareUnits * kUnit);
+    if (s > 512 / rows) s = 512 / rows;
+    if (s > kMostShares) s = kMostShares;
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
@@ -205,25 +546,47 @@ int shares_of(int64_t rows, int64_t vocab)
 
 size_t policy_scratch(int64_t rows, int64_t vocab)
 {
-    return static_cast<size_t>(rows) * (shares_of(rows, vocab) * sizeof(Share) + sizeof(double));
+    const int shares = shares_of(rows, vocab);
+    if (shares > 1) return static_cast<size_t>(rows) * (shares * sizeof(Share) + sizeof(double));
+    return static_cast<size_t>(rows < kMostBlocks ? rows : kMostBlocks) * sizeof(double);
 }
 
 hipError_t launch_policy_loss(const PolicyArgs& a, bool bf16, void* scratch, hipStream_t stream)
 {
     const int shares = shares_of(a.rows, a.vocab);
-    Share* parts = static_cast<Share*>(scratch);
-    double* row_loss = a.loss ? reinterpret_cast<double*>(parts + a.rows * shares) : nullptr;
-    if (a.rows > 0) {
-        const dim3 grid(static_cast<uint32_t>(a.rows < kMostRowBlocks ? a.rows : kMostRowBlocks), shares);
+    double* losses = static_cast<double*>(scratch);
+    int64_t n = 0;  // their count
+    auto blocks = [&](int64_t jobs, int most) { return static_cast<int>(n = jobs < most ? jobs : most); };
+    if (a.rows > 0 && shares > 1) {
+        Share* parts = static_cast<Share*>(scratch);
+        losses = reinterpret_cast<double*>(parts + a.rows * shares);
+        const dim3 grid(static_cast<uint32_t>(n = a.rows), shares);
         if (bf16) {
             policy_shares_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts);
-            policy_rows_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts, row_loss);
+            policy_rows_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts, a.loss ? losses : nullptr);
         } else {
             policy_shares_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts);
-            policy_rows_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts, row_loss);
+            policy_rows_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts, a.loss ? losses : nullptr);
+        }
+    } else if (a.rows > 0 && a.vocab <= kWaveVocab) {
+        const int grid = blocks((a.rows + kGroup - 1) / kGroup, kMostBlocks);
+        if (bf16) policy_wave_kernel<true><<<grid, kBlock, 0, stream>>>(a, a.loss ? losses : nullptr);
+        else policy_wave_kernel<false><<<grid, kBlock, 0, stream>>>(a, a.loss ? losses : nullptr);
+    } else if (a.rows > 0) {
+        double* l = a.loss ? losses : nullptr;
+        if (a.vocab <= kBlockVocab) {
+            const int grid = blocks(a.rows, kMostBlocks);
+            if (bf16) policy_block_kernel<true><<<grid, kBlock, 0, stream>>>(a, l);
+            else policy_block_kernel<false><<<grid, kBlock, 0, stream>>>(a, l);
+        } else if (bf16) {
+            if (a.vocab < 1024 * 8 * 8) policy_kept_kernel<true, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, l);
+            else policy_kept_kernel<true, 1024, 8, 8><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, l);
+        } else {
+            if (a.vocab < 1024 * 4 * 8) policy_kept_kernel<false, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, l);
+            else policy_kept_kernel<false, 1024, 4, 4><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, l);
         }
     }
-    if (a.loss) policy_total_kernel<<<1, kBlock, 0, stream>>>(row_loss, a.rows, a.loss);
+    if (a.loss) policy_total_kernel<<<1, kBlock, 0, stream>>>(losses, n, a.loss);
     return hipGetLastError();
 }
 

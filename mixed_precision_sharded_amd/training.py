@@ -62,52 +62,70 @@ def _function(name: str):
     return _functions[name]
 
 
+# The current stream's handle without building a Stream object, where torch
+# offers it (a call's checks cost the host about as much as its launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _enqueue(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
     """Call an entry point on `stream` with the tensors' device current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream: of {stream.device}, with tensors on {device}")
-    f = _function(name)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream: of {stream.device}, with tensors on {device}")
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    f = _functions[name] if _bound is binding._lib and _bound is not None else _function(name)
     if torch.cuda.current_device() == device.index:
-        rc = f(*args, stream.cuda_stream)
+        rc = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, stream.cuda_stream)
+            rc = f(*args, handle)
     if rc:
         binding._check(rc, name)
 
 
-def _matrix_type(t: torch.Tensor, name: str) -> int:
-    """The C dtype of the matrix that fixes a call's type, shape and device."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: a matrix, got {t.dim()} dimensions")
+def _matrix(t: torch.Tensor, name: str):
+    """(C dtype, rows, cols, row stride) of the matrix that fixes a call's type,
+    shape and device."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: a matrix, got {len(shape)} dimensions")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be on a CUDA device, got {t.device}")
-    if t.dtype == torch.bfloat16:
-        return MPS_DTYPE_BF16
-    if t.dtype == torch.float32:
-        return MPS_DTYPE_F32
-    raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        kind = MPS_DTYPE_BF16
+    elif dtype is torch.float32:
+        kind = MPS_DTYPE_F32
+    else:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {dtype}")
+    return kind, shape[0], shape[1], _row_stride(t, shape[0], shape[1], name)
+
+
+def _row_stride(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
+    down, across = t.stride()
+    if across != 1 and cols > 1 and rows:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return down if rows > 1 else cols  # one row: its stride says nothing
 
 
 def _rows(t: torch.Tensor, like: torch.Tensor, shape, name: str) -> int:
     """The row stride of a matrix of `like`'s type and device."""
-    if t.dtype != like.dtype:
+    if t.dtype is not like.dtype:
         raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name}: must be on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-    rows, cols = shape
-    if cols > 1 and rows and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if rows > 1 else cols
+    return _row_stride(t, shape[0], shape[1], name)
 
 
 def _flat(t: torch.Tensor, dtype, shape, device, name: str) -> int:
     """The address of a contiguous tensor of this type and shape."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: must be on {device}")
@@ -119,15 +137,15 @@ def _flat(t: torch.Tensor, dtype, shape, device, name: str) -> int:
 
 
 def _kept(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, device, name: str = ""):
-    row = act8_row(cols)
-    return (_flat(codes, torch.uint8, (rows, row), device, name + "codes"),
-            _flat(scales, torch.uint8, (rows, row // MPS_Q8_BLOCK), device, name + "scales"))
+    runs = (cols + MPS_Q8_BLOCK - 1) // MPS_Q8_BLOCK
+    return (_flat(codes, torch.uint8, (rows, runs * MPS_Q8_BLOCK), device, name + "codes"),
+            _flat(scales, torch.uint8, (rows, runs), device, name + "scales"))
 
 
 def _workspace(t: Optional[torch.Tensor], device):
     if t is None:
         return None, 0
-    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace: contiguous uint8 tensor on {device}")
     return t.data_ptr(), t.numel()
 
@@ -149,20 +167,20 @@ def act8_empty(rows: int, cols: int, device) -> tuple:
 def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """Keep the matrix x in 8 bits; returns (codes, scales)."""
-    kind = _matrix_type(x, "x")
-    rows, cols = x.shape
-    _enqueue("act8_save", x.device, stream, x.data_ptr(), kind, _rows(x, x, x.shape, "x"), rows, cols,
-             *_kept(codes, scales, rows, cols, x.device))
+    kind, rows, cols, stride = _matrix(x, "x")
+    dev = x.device
+    _enqueue("act8_save", dev, stream, x.data_ptr(), kind, stride, rows, cols,
+             *_kept(codes, scales, rows, cols, dev))
     return codes, scales
 
 
 def act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The values that codes and scales stand for, in out's type."""
-    kind = _matrix_type(out, "out")
-    rows, cols = out.shape
-    _enqueue("act8_load", out.device, stream, *_kept(codes, scales, rows, cols, out.device), rows, cols,
-             out.data_ptr(), kind, _rows(out, out, out.shape, "out"))
+    kind, rows, cols, stride = _matrix(out, "out")
+    dev = out.device
+    _enqueue("act8_load", dev, stream, *_kept(codes, scales, rows, cols, dev), rows, cols,
+             out.data_ptr(), kind, stride)
     return out
 
 
@@ -171,10 +189,9 @@ def act8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: torch.T
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out = x * rstd * weight per row, rstd = 1 / sqrt(mean(x^2) + eps) (float32,
     one per row); x is kept in codes and scales.  weight: float32."""
-    kind = _matrix_type(x, "x")
-    rows, cols = x.shape
+    kind, rows, cols, stride = _matrix(x, "x")
     dev = x.device
-    _enqueue("act8_rmsnorm", dev, stream, x.data_ptr(), kind, _rows(x, x, x.shape, "x"), rows, cols,
+    _enqueue("act8_rmsnorm", dev, stream, x.data_ptr(), kind, stride, rows, cols,
              _flat(weight, torch.float32, (cols,), dev, "weight"), float(eps), out.data_ptr(),
              _rows(out, x, x.shape, "out"), _flat(rstd, torch.float32, (rows,), dev, "rstd"),
              *_kept(codes, scales, rows, cols, dev))
@@ -195,15 +212,14 @@ def act8_rmsnorm_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.T
     """dx and dweight (float32; added to with accumulate) of act8_rmsnorm from dy
     and the kept x and rstd; dx gets residual_grad added, and out_codes and
     out_scales, if given, the norm's output again in 8 bits."""
-    kind = _matrix_type(dy, "dy")
-    rows, cols = dy.shape
+    kind, rows, cols, stride = _matrix(dy, "dy")
     dev = dy.device
     if (out_codes is None) != (out_scales is None):
         raise ValueError("out_codes and out_scales: both or neither")
     res = (None, 0) if residual_grad is None else (residual_grad.data_ptr(),
                                                    _rows(residual_grad, dy, dy.shape, "residual_grad"))
     again = (None, None) if out_codes is None else _kept(out_codes, out_scales, rows, cols, dev, "out_")
-    _enqueue("act8_rmsnorm_backward", dev, stream, dy.data_ptr(), kind, _rows(dy, dy, dy.shape, "dy"),
+    _enqueue("act8_rmsnorm_backward", dev, stream, dy.data_ptr(), kind, stride,
              *_kept(codes, scales, rows, cols, dev), _flat(rstd, torch.float32, (rows,), dev, "rstd"),
              rows, cols, _flat(weight, torch.float32, (cols,), dev, "weight"), *res, dx.data_ptr(),
              _rows(dx, dy, dy.shape, "dx"), _flat(dweight, torch.float32, (cols,), dev, "dweight"),
@@ -215,10 +231,9 @@ def act8_swiglu(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor, gate_co
                 gate_scales: torch.Tensor, up_codes: torch.Tensor, up_scales: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out = gate * sigmoid(gate) * up; gate and up are kept in 8 bits."""
-    kind = _matrix_type(gate, "gate")
-    rows, cols = gate.shape
+    kind, rows, cols, stride = _matrix(gate, "gate")
     dev = gate.device
-    _enqueue("act8_swiglu", dev, stream, gate.data_ptr(), _rows(gate, gate, gate.shape, "gate"),
+    _enqueue("act8_swiglu", dev, stream, gate.data_ptr(), stride,
              up.data_ptr(), _rows(up, gate, gate.shape, "up"), kind, rows, cols, out.data_ptr(),
              _rows(out, gate, gate.shape, "out"), *_kept(gate_codes, gate_scales, rows, cols, dev, "gate_"),
              *_kept(up_codes, up_scales, rows, cols, dev, "up_"))
@@ -232,14 +247,13 @@ def act8_swiglu_backward(dout: torch.Tensor, gate_codes: torch.Tensor, gate_scal
                          stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """(dgate, dup) of act8_swiglu from dout and the kept gate and up; out_codes
     and out_scales, if given, get the forward output again in 8 bits."""
-    kind = _matrix_type(dout, "dout")
-    rows, cols = dout.shape
+    kind, rows, cols, stride = _matrix(dout, "dout")
     dev = dout.device
     if (out_codes is None) != (out_scales is None):
         raise ValueError("out_codes and out_scales: both or neither")
     again = (None, None) if out_codes is None else _kept(out_codes, out_scales, rows, cols, dev, "out_")
     _enqueue("act8_swiglu_backward", dev, stream, dout.data_ptr(), kind,
-             _rows(dout, dout, dout.shape, "dout"), *_kept(gate_codes, gate_scales, rows, cols, dev, "gate_"),
+             stride, *_kept(gate_codes, gate_scales, rows, cols, dev, "gate_"),
              *_kept(up_codes, up_scales, rows, cols, dev, "up_"), rows, cols, dgate.data_ptr(),
              _rows(dgate, dout, dout.shape, "dgate"), dup.data_ptr(), _rows(dup, dout, dout.shape, "dup"),
              *again)
@@ -255,12 +269,10 @@ def act8_weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """dw[out_features, in_features] (float32 or bfloat16, contiguous; added to with
     accumulate) = dy^T x, x the kept activation [tokens, in_features]."""
-    kind = _matrix_type(dy, "dy")
-    dw_kind = _matrix_type(dw, "dw")
-    tokens, n = dy.shape
-    k = dw.shape[1]
+    kind, tokens, n, stride = _matrix(dy, "dy")
+    dw_kind, _, k, _ = _matrix(dw, "dw")
     dev = dy.device
-    _enqueue("act8_weight_grad", dev, stream, dy.data_ptr(), kind, _rows(dy, dy, dy.shape, "dy"),
+    _enqueue("act8_weight_grad", dev, stream, dy.data_ptr(), kind, stride,
              *_kept(codes, scales, tokens, k, dev), tokens, n, k, _flat(dw, dw.dtype, (n, k), dev, "dw"),
              dw_kind, 1 if accumulate else 0, *_workspace(workspace, dev))
     return dw
@@ -283,15 +295,14 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
     KL term, and with dlogits (logits' type; may be logits itself) the gradient.
     labels: int64; the other vectors float32, one value per row.  Rows with a
     label outside the vocabulary or a weight of 0 are left out."""
-    kind = _matrix_type(logits, "logits")
-    rows, vocab = logits.shape
+    kind, rows, vocab, stride = _matrix(logits, "logits")
     dev = logits.device
 
     def vector(t, name):
         return None if t is None else _flat(t, torch.float32, (rows,), dev, name)
 
     d = (None, 0) if dlogits is None else (dlogits.data_ptr(), _rows(dlogits, logits, logits.shape, "dlogits"))
-    _enqueue("policy_loss", dev, stream, logits.data_ptr(), kind, _rows(logits, logits, logits.shape, "logits"),
+    _enqueue("policy_loss", dev, stream, logits.data_ptr(), kind, stride,
              rows, vocab, _flat(labels, torch.int64, (rows,), dev, "labels"), vector(old_logp, "old_logp"),
              vector(ref_logp, "ref_logp"), vector(advantage, "advantage"), vector(weight, "weight"),
              float(clip_low), float(clip_high), float(kl_coef), _flat(loss, torch.float32, (1,), dev, "loss"),
@@ -303,11 +314,10 @@ def token_logprobs(logits: torch.Tensor, labels: torch.Tensor, out: torch.Tensor
                    workspace: Optional[torch.Tensor],
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out (float32, one per row) = logits[label] - logsumexp(logits)."""
-    kind = _matrix_type(logits, "logits")
-    rows, vocab = logits.shape
+    kind, rows, vocab, stride = _matrix(logits, "logits")
     dev = logits.device
     _enqueue("token_logprobs", dev, stream, logits.data_ptr(), kind,
-             _rows(logits, logits, logits.shape, "logits"), rows, vocab,
+             stride, rows, vocab,
              _flat(labels, torch.int64, (rows,), dev, "labels"), _flat(out, torch.float32, (rows,), dev, "out"),
              *_workspace(workspace, dev))
     return out
