@@ -153,9 +153,8 @@ struct Running {
     }
 };
 
-// The whole units of (a stretch of) a row, through a buffer resource: one
-// 32-bit offset per thread and a constant per access, where pointers would
-// take two registers each.  A unit behind the last one reads as zeros and is
+// The whole units of (a stretch of) a row, through a buffer resource: a 32-bit
+// offset per access, where a pointer would take two registers.  A unit behind the last one reads as zeros and is
 // not stored.
 template <bool kBf16>
 struct Units {
@@ -167,40 +166,44 @@ struct Units {
     {
     }
 
-    // Unit `unit` + `more`, the second the same in every lane.
-    __device__ __forceinline__ Raw8<kBf16> load(uint32_t unit, uint32_t more) const
+    // Every offset is in the vector operand.  A scalar offset does not take
+    // part in the resource's bounds check; and 16-byte stores with a scalar
+    // offset in a register were seen to send data that the next instructions
+    // had already overwritten (the compiler leaves the one wait state out that
+    // it puts behind a store without one).
+    __device__ __forceinline__ Raw8<kBf16> load(uint32_t unit) const
     {
         Raw8<kBf16> v;
-        v.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes, more * kBytes, kLogitsPolicy);
-        if (!kBf16) v.v[kBf16 ? 0 : 1] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes + 16, more * kBytes, kLogitsPolicy);
+        v.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes, 0, kLogitsPolicy);
+        if (!kBf16) v.v[kBf16 ? 0 : 1] = __builtin_amdgcn_raw_buffer_load_b128(r, unit * kBytes + 16, 0, kLogitsPolicy);
         return v;
     }
 
-    __device__ __forceinline__ void store(const float (&x)[kUnit], uint32_t unit, uint32_t more) const
+    __device__ __forceinline__ void store(const float (&x)[kUnit], uint32_t unit) const
     {
         if (kBf16) {
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = bf16_pack2(x[2 * i], x[2 * i + 1]);
-            __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes, more * kBytes, kGradientPolicy);
+            __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes, 0, kGradientPolicy);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const u32x4 w = {__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), __float_as_uint(x[4 * h + 2]),
                                  __float_as_uint(x[4 * h + 3])};
-                __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes + 16 * h, more * kBytes, kGradientPolicy);
+                __builtin_amdgcn_raw_buffer_store_b128(w, r, unit * kBytes + 16 * h, 0, kGradientPolicy);
             }
         }
     }
 
     // Stores factor * e^(x - top) of a unit.
-    __device__ __forceinline__ void give(const Raw8<kBf16>& raw, float factor, float top, uint32_t unit, uint32_t more) const
+    __device__ __forceinline__ void give(const Raw8<kBf16>& raw, float factor, float top, uint32_t unit) const
     {
         float x[kUnit];
         widen<kBf16>(raw, x);
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) x[i] = factor * exp_below(x[i], top);
-        store(x, unit, more);
+        store(x, unit);
     }
 };
 
@@ -226,11 +229,11 @@ __device__ __forceinline__ Share read_share(const PolicyArgs& a, int64_t row, in
     for (; u + (kDeep - 1) * kTeam < full; u += kDeep * kTeam) {
         Raw8<kBf16> raw[kDeep];
 #pragma unroll
-        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u, v * kTeam);
+        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u + v * kTeam);
 #pragma unroll
         for (int v = 0; v < kDeep; ++v) run.take(raw[v]);
     }
-    for (; u < full; u += kTeam) run.take(in.load(u, 0));
+    for (; u < full; u += kTeam) run.take(in.load(u));
     Share s = {run.top, static_cast<double>(run.sum)};
     if (t < static_cast<int>(count % kUnit)) {
         const float x = logit_at(a, kBf16, row * a.logits.stride + first + full * kUnit + t);
@@ -253,7 +256,7 @@ __device__ __forceinline__ void write_gradient(const PolicyArgs& a, int64_t row,
     uint32_t u = t;
     if (r.slope == 0.0f && factor == 0.0f) {  // zeros, whatever the logits
         const float x[kUnit] = {};
-        for (; u < full; u += kTeam) out.store(x, u, 0);
+        for (; u < full; u += kTeam) out.store(x, u);
         if (t < static_cast<int>(count % kUnit)) store_logit(a, kBf16, to + full * kUnit + t, 0.0f);
         return;
     }
@@ -261,11 +264,11 @@ __device__ __forceinline__ void write_gradient(const PolicyArgs& a, int64_t row,
     for (; u + (kDeep - 1) * kTeam < full; u += kDeep * kTeam) {
         Raw8<kBf16> raw[kDeep];
 #pragma unroll
-        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u, v * kTeam);
+        for (int v = 0; v < kDeep; ++v) raw[v] = in.load(u + v * kTeam);
 #pragma unroll
-        for (int v = 0; v < kDeep; ++v) out.give(raw[v], factor, top, u, v * kTeam);
+        for (int v = 0; v < kDeep; ++v) out.give(raw[v], factor, top, u + v * kTeam);
     }
-    for (; u < full; u += kTeam) out.give(in.load(u, 0), factor, top, u, 0);
+    for (; u < full; u += kTeam) out.give(in.load(u), factor, top, u);
     if (t < static_cast<int>(count % kUnit)) {
         const int64_t c = full * kUnit + t;
         store_logit(a, kBf16, to + c, factor * exp_below(logit_at(a, kBf16, row * a.logits.stride + first + c), top));
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, dou
     Raw8<kBf16> reg[kRegs];
     auto load_regs = [&](const Units<kBf16>& in) {
 #pragma unroll
-        for (int j = 0; j < kRegs; ++j) reg[j] = in.load(t, j * kThreads);
+        for (int j = 0; j < kRegs; ++j) reg[j] = in.load(t + j * kThreads);
     };
     int64_t row = blockIdx.x;
     bool live = row < a.rows && row_live(a, row);
@@ -349,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, dou
             Running run;
             Raw8<kBf16> raw[kHalf];
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) raw[j] = in.load(t, (kRegs + j) * kThreads);
+            for (int j = 0; j < kHalf; ++j) raw[j] = in.load(t + (kRegs + j) * kThreads);
 #pragma unroll
             for (int j = 0; j < kRegs; ++j) run.take(reg[j]);  // whole: the row has as many units
 #pragma unroll
@@ -359,10 +362,10 @@ __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, dou
                     const int at = h * kHalf + j;
                     for (int w = 0; w < kWords; ++w) kept[(at * kWords + w) * kThreads + t] = raw[j].v[w];
                     if (t + (kRegs + at) * kThreads < full) run.take(raw[j]);
-                    if (h == 0) raw[j] = in.load(t, (kRegs + kHalf + j) * kThreads);
+                    if (h == 0) raw[j] = in.load(t + (kRegs + kHalf + j) * kThreads);
                 }
             }
-            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) run.take(in.load(u, 0));
+            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) run.take(in.load(u));
             s = {run.top, static_cast<double>(run.sum)};
             if (t < rest) {
                 const float x = logit_at(a, kBf16, row * a.logits.stride + full * kUnit + t);
@@ -383,16 +386,16 @@ __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, dou
 #pragma unroll
             for (int j = 0; j < kRegs; ++j) {
                 forget(reg[j]);
-                out.give(reg[j], factor, top, t, j * kThreads);
-                if (next_live) reg[j] = coming.load(t, j * kThreads);
+                out.give(reg[j], factor, top, t + j * kThreads);
+                if (next_live) reg[j] = coming.load(t + j * kThreads);
             }
 #pragma unroll
             for (int j = 0; j < kLds; ++j) {
                 Raw8<kBf16> raw;
                 for (int w = 0; w < kWords; ++w) raw.v[w] = kept[(j * kWords + w) * kThreads + t];
-                out.give(raw, factor, top, t, (kRegs + j) * kThreads);
+                out.give(raw, factor, top, t + (kRegs + j) * kThreads);
             }
-            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) out.give(in.load(u, 0), factor, top, u, 0);
+            for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) out.give(in.load(u), factor, top, u);
             if (t < rest) {
                 const int64_t c = full * kUnit + t;
                 store_logit(a, kBf16, to + c, factor * exp_below(logit_at(a, kBf16, row * a.logits.stride + c), top));
