@@ -95,6 +95,12 @@ __device__ __forceinline__ void store_logit(const PolicyArgs& a, bool bf16, int6
     else static_cast<float*>(a.dlogits.data)[i] = v;
 }
 
+// The logit of a live row's label.
+__device__ __forceinline__ float label_logit_of(const PolicyArgs& a, bool bf16, int64_t row)
+{
+    return logit_at(a, bf16, row * a.logits.stride + a.labels[row]);
+}
+
 // Whether a row takes part at all.
 __device__ __forceinline__ bool row_live(const PolicyArgs& a, int64_t row)
 {
@@ -102,14 +108,14 @@ __device__ __forceinline__ bool row_live(const PolicyArgs& a, int64_t row)
     return label >= 0 && label < a.vocab && !(a.weight && a.weight[row] == 0.0f);
 }
 
-// The result of a live row whose share this is, and its own outputs; one lane
-// per row.
-__device__ __forceinline__ RowResult finish_row(const PolicyArgs& a, bool bf16, int64_t row, bool live, const Share& s)
+// The result of a live row whose share and label's logit these are, and its
+// own outputs; one lane per row.
+__device__ __forceinline__ RowResult finish_row(const PolicyArgs& a, int64_t row, bool live, const Share& s, float label_logit)
 {
     RowResult r = {};
     if (live) {
         const bool loss_too = a.loss != nullptr, with_ref = a.ref_logp != nullptr;
-        r = row_values(s.top, s.sum, logit_at(a, bf16, row * a.logits.stride + a.labels[row]), loss_too, with_ref,
+        r = row_values(s.top, s.sum, label_logit, loss_too, with_ref,
                        loss_too ? a.old_logp[row] : 0.0f, with_ref ? a.ref_logp[row] : 0.0f, loss_too ? a.advantage[row] : 0.0f,
                        loss_too ? a.weight[row] : 0.0f, 1.0 - a.clip_low, 1.0 + a.clip_high, a.kl_coef);
     }
@@ -297,7 +303,7 @@ __device__ __forceinline__ void finish_block(const PolicyArgs& a, int64_t row, b
     if (wave == 0) {
         const Share s = lanes_join<kWaves>(shares[lane % kWaves]);
         if (lane == 0) {
-            *result = finish_row(a, kBf16, row, live, s);
+            *result = finish_row(a, row, live, s, live ? label_logit_of(a, kBf16, row) : 0.0f);
             total += result->loss;
         }
     }
@@ -434,7 +440,8 @@ __global__ __launch_bounds__(kBlock) void policy_wave_kernel(PolicyArgs a, doubl
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < n) {
             const int64_t row = first + threadIdx.x;
-            results[threadIdx.x] = finish_row(a, kBf16, row, row_live(a, row), shares[threadIdx.x]);
+            const bool live = row_live(a, row);
+            results[threadIdx.x] = finish_row(a, row, live, shares[threadIdx.x], live ? label_logit_of(a, kBf16, row) : 0.0f);
         }
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -461,49 +468,59 @@ __device__ __forceinline__ Span span_of(int64_t vocab, int shares, int share)
     return {min(per * share, vocab), min(per * (share + 1), vocab)};
 }
 
-// Shares of every row: block (row, share).
+// Shares of every row: block (row, share).  The label's logit is kept as well:
+// the next kernel's blocks may write the gradient over the logits while others
+// of the same row have yet to compute its result.
 template <bool kBf16>
-__global__ __launch_bounds__(kBlock) void policy_shares_kernel(PolicyArgs a, int shares, Share* out)
+__global__ __launch_bounds__(kBlock) void policy_shares_kernel(PolicyArgs a, int shares, Share* out, float* label_logits)
 {
     __shared__ Share lds[kWavesPerBlock];
     const Span span = span_of(a.vocab, shares, blockIdx.y);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        if (!row_live(a, row)) continue;
-        Share s = lanes_join<kWave>(read_share<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x));
-        __syncthreads();
-        if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
-        __syncthreads();
-        if (threadIdx.x < kWave) {
-            s = lanes_join<kWavesPerBlock>(lds[threadIdx.x % kWavesPerBlock]);
-            if (threadIdx.x == 0) out[row * shares + blockIdx.y] = s;
-        }
+    const int64_t row = blockIdx.x;
+    if (!row_live(a, row)) return;
+    if (blockIdx.y == 0 && threadIdx.x == 0) label_logits[row] = label_logit_of(a, kBf16, row);
+    Share s = lanes_join<kWave>(read_share<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x));
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        s = lanes_join<kWavesPerBlock>(lds[threadIdx.x % kWavesPerBlock]);
+        if (threadIdx.x == 0) out[row * shares + blockIdx.y] = s;
     }
 }
 
 // Joins the (at most 64) shares of a row, and writes this block's part of the
-// gradient; the first share's block writes the row's own results.
+// gradient; the first share's block writes the row's own results, and the
+// second wavefront of the very first block computes every row's loss once
+// more, a row (of at most 64) per lane, for their sum.
 template <bool kBf16>
-__global__ __launch_bounds__(kBlock) void policy_rows_kernel(PolicyArgs a, int shares, const Share* in, double* losses)
+__global__ __launch_bounds__(kBlock) void policy_rows_kernel(PolicyArgs a, int shares, const Share* in, const float* label_logits)
 {
     __shared__ RowResult result;
     const Span span = span_of(a.vocab, shares, blockIdx.y);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        __syncthreads();
-        if (threadIdx.x < kWave) {
-            const bool live = row_live(a, row);
-            const int lane = threadIdx.x;
-            const Share s = lanes_join<kWave>(live && lane < shares ? in[row * shares + lane] : Share{-INFINITY, 0.0});
-            if (lane == 0) {
-                // Every block computes the row's values; the first one's are kept.
-                PolicyArgs mine = a;
-                if (blockIdx.y != 0) mine.token_logp = mine.token_kl = nullptr;
-                result = finish_row(mine, kBf16, row, live, s);
-                if (blockIdx.y == 0 && losses) losses[row] = result.loss;
-            }
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    if (wave == 0) {
+        const bool live = row_live(a, row);
+        const Share s = lanes_join<kWave>(live && lane < shares ? in[row * shares + lane] : Share{-INFINITY, 0.0});
+        if (lane == 0) {
+            PolicyArgs mine = a;
+            if (blockIdx.y != 0) mine.token_logp = mine.token_kl = nullptr;
+            result = finish_row(mine, row, live, s, live ? label_logits[row] : 0.0f);
         }
-        __syncthreads();
-        if (a.dlogits.data) write_gradient<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x, result, a.labels[row]);
+    } else if (wave == 1 && a.loss && blockIdx.x == 0 && blockIdx.y == 0) {
+        double loss = 0.0;
+        if (lane < a.rows && row_live(a, lane)) {
+            Share s = in[lane * shares];
+            for (int i = 1; i < shares; ++i) s = join(s, in[lane * shares + i]);
+            PolicyArgs mine = a;
+            mine.token_logp = mine.token_kl = nullptr;
+            loss = finish_row(mine, lane, true, s, label_logits[lane]).loss;
+        }
+        loss = wave_sum(loss);
+        if (lane == 0) *a.loss = static_cast<float>(loss);
     }
+    __syncthreads();
+    if (a.dlogits.data) write_gradient<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x, result, a.labels[row]);
 }
 
 // *loss = the n values' sum, in a fixed order.
@@ -526,23 +543,25 @@ __global__ __launch_bounds__(kBlock) void policy_total_kernel(const double* valu
 //   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 30 against
 //     34, 8192 x 128256 bf16 811 against 1200, 2000 x 65000 fp32 231 against
 //     315; 1000 x 32003 fp32 58 against 75;
-//   - up to kFewRows rows, blocks share a row: 24 x 128256 bf16 19 against 22.
+//   - up to kFewRows rows of more than kShareVocab logits, blocks share a row:
+//     24 x 128256 bf16 14.9 against 18.8, 64 x 200000 18.6 against 28.8; but
+//     24 x 50257 14.9 against 13.7, 128 x 128256 22.6 against 20.1.
 constexpr int64_t kWaveVocab = 8192;
 constexpr int64_t kBlockVocab = 16384;
 constexpr int64_t kFewRows = 64;
-constexpr int kShareUnits = 1024;  // units of eight logits in a share, at least
-constexpr int kMostShares = kWave;
+constexpr int64_t kShareVocab = 65536;
+constexpr int kShareLogits = 8192;  // in a share, at least
 constexpr int kMostBlocks = 2048;
+static_assert(kFewRows <= kWave, "a row per lane");
 
-// Blocks that share a row, where rows are few and long: two blocks per CU in
-// all.  1: a row per block or per wavefront.
+// Blocks that share a row: two blocks per CU in all, and at most a lane's
+// worth.  1: a row per block or per wavefront.
 int shares_of(int64_t rows, int64_t vocab)
 {
-    if (rows <= 0 || rows > kFewRows) return 1;
-    int64_t s = vocab / (kShareUnits * kUnit);
+    if (rows <= 0 || rows > kFewRows || vocab <= kShareVocab) return 1;
+    int64_t s = vocab / kShareLogits;
     if (s > 512 / rows) s = 512 / rows;
-    if (s > kMostShares) s = kMostShares;
-    return static_cast<int>(s < 1 ? 1 : s);
+    return static_cast<int>(s > kWave ? kWave : s);
 }
 
 }  // namespace
@@ -550,43 +569,44 @@ int shares_of(int64_t rows, int64_t vocab)
 size_t policy_scratch(int64_t rows, int64_t vocab)
 {
     const int shares = shares_of(rows, vocab);
-    if (shares > 1) return static_cast<size_t>(rows) * (shares * sizeof(Share) + sizeof(double));
+    if (shares > 1) return static_cast<size_t>(rows) * (shares * sizeof(Share) + sizeof(float));
     return static_cast<size_t>(rows < kMostBlocks ? rows : kMostBlocks) * sizeof(double);
 }
 
 hipError_t launch_policy_loss(const PolicyArgs& a, bool bf16, void* scratch, hipStream_t stream)
 {
     const int shares = shares_of(a.rows, a.vocab);
-    double* losses = static_cast<double*>(scratch);
-    int64_t n = 0;  // their count
-    auto blocks = [&](int64_t jobs, int most) { return static_cast<int>(n = jobs < most ? jobs : most); };
-    if (a.rows > 0 && shares > 1) {
+    if (shares > 1) {
         Share* parts = static_cast<Share*>(scratch);
-        losses = reinterpret_cast<double*>(parts + a.rows * shares);
-        const dim3 grid(static_cast<uint32_t>(n = a.rows), shares);
+        float* label_logits = reinterpret_cast<float*>(parts + a.rows * shares);
+        const dim3 grid(static_cast<uint32_t>(a.rows), shares);
         if (bf16) {
-            policy_shares_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts);
-            policy_rows_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts, a.loss ? losses : nullptr);
+            policy_shares_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts, label_logits);
+            policy_rows_kernel<true><<<grid, kBlock, 0, stream>>>(a, shares, parts, label_logits);
         } else {
-            policy_shares_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts);
-            policy_rows_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts, a.loss ? losses : nullptr);
+            policy_shares_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts, label_logits);
+            policy_rows_kernel<false><<<grid, kBlock, 0, stream>>>(a, shares, parts, label_logits);
         }
-    } else if (a.rows > 0 && a.vocab <= kWaveVocab) {
+        return hipGetLastError();
+    }
+    double* losses = a.loss ? static_cast<double*>(scratch) : nullptr;  // a sum per block
+    int64_t n = 0;                                                      // their count
+    auto blocks = [&](int64_t jobs, int most) { return static_cast<int>(n = jobs < most ? jobs : most); };
+    if (a.rows > 0 && a.vocab <= kWaveVocab) {
         const int grid = blocks((a.rows + kGroup - 1) / kGroup, kMostBlocks);
-        if (bf16) policy_wave_kernel<true><<<grid, kBlock, 0, stream>>>(a, a.loss ? losses : nullptr);
-        else policy_wave_kernel<false><<<grid, kBlock, 0, stream>>>(a, a.loss ? losses : nullptr);
+        if (bf16) policy_wave_kernel<true><<<grid, kBlock, 0, stream>>>(a, losses);
+        else policy_wave_kernel<false><<<grid, kBlock, 0, stream>>>(a, losses);
     } else if (a.rows > 0) {
-        double* l = a.loss ? losses : nullptr;
         if (a.vocab <= kBlockVocab) {
             const int grid = blocks(a.rows, kMostBlocks);
-            if (bf16) policy_block_kernel<true><<<grid, kBlock, 0, stream>>>(a, l);
-            else policy_block_kernel<false><<<grid, kBlock, 0, stream>>>(a, l);
+            if (bf16) policy_block_kernel<true><<<grid, kBlock, 0, stream>>>(a, losses);
+            else policy_block_kernel<false><<<grid, kBlock, 0, stream>>>(a, losses);
         } else if (bf16) {
-            if (a.vocab < 1024 * 8 * 8) policy_kept_kernel<true, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, l);
-            else policy_kept_kernel<true, 1024, 8, 8><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, l);
+            if (a.vocab < 1024 * 8 * 8) policy_kept_kernel<true, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, losses);
+            else policy_kept_kernel<true, 1024, 8, 8><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, losses);
         } else {
-            if (a.vocab < 1024 * 4 * 8) policy_kept_kernel<false, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, l);
-            else policy_kept_kernel<false, 1024, 4, 4><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, l);
+            if (a.vocab < 1024 * 4 * 8) policy_kept_kernel<false, 512, 4, 4><<<blocks(a.rows, 256 * 2), 512, 0, stream>>>(a, losses);
+            else policy_kept_kernel<false, 1024, 4, 4><<<blocks(a.rows, 256), 1024, 0, stream>>>(a, losses);
         }
     }
     if (a.loss) policy_total_kernel<<<1, kBlock, 0, stream>>>(losses, n, a.loss);
