@@ -49,7 +49,7 @@
  *     graphs that may be replayed at the same time).
  *   - Results do not depend on the order in which the device runs blocks:
  *     the same call on the same data gives the same bits.
- *   - Sizes: 0 <= rows (tokens) < 2^31, 1 <= cols (features, vocab) <= 2^28,
+ *   - Sizes: 0 <= rows (tokens) < 2^31, 1 <= cols (features, vocab) <= 2^27,
  *     strides below 2^31; a matrix may have more than 2^32 elements.
  */
 #ifndef MPS_TRAIN_H

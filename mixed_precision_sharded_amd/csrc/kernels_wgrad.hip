@@ -23,56 +23,66 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTileT = 32;   // t per stage: two matrix instructions deep
-constexpr int kTile = 128;   // rows (n) and columns (k) of a block's tile
+constexpr int kStageBf16 = 64, kStageF32 = 32;  // t per stage of the tiles of 128 and 64
 constexpr int kFrag = 32;    // rows and columns of one matrix instruction
 
-// Byte offset in a staged tile [kTileT][kTile] of bf16 of the 16-byte chunk
+// Byte offset in a staged tile [t][kCols] of bf16 of the 16-byte chunk
 // `chunk` of row t.  A transposing load reads 32 bytes from each of four
 // consecutive rows per 16 lanes; the exclusive-or sends the four rows to
-// different banks.
+// different banks (rows of 64 columns lie two to the banks' 256 bytes).
+template <int kCols>
 __device__ __forceinline__ uint32_t chunk_at(int t, int chunk)
 {
-    return static_cast<uint32_t>(t * kTile * 2 + ((chunk ^ ((t & 3) << 2)) << 4));
+    const int mixed = kCols == 64 ? chunk ^ ((t & 2) << 1) : chunk ^ ((t & 3) << 2);
+    return static_cast<uint32_t>(t * kCols * 2 + (mixed << 4));
 }
 
 // Four t (t0 .. t0 + 3) of column `col` for each lane of a group of 16, whose
 // lanes hold 16 consecutive columns from col0 on.
+template <int kCols>
 __device__ __forceinline__ bf16x4 read_transposed(const char* tile, int t0, int col0, int lane16)
 {
     const int t = t0 + lane16 / 4;
     const int col = col0 + lane16 % 4 * 4;
-    const char* p = tile + chunk_at(t, col / 8) + (col % 8) * 2;
+    const char* p = tile + chunk_at<kCols>(t, col / 8) + (col % 8) * 2;
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                           (__attribute__((address_space(3))) s16x4*)p));
 }
 
 // The operand of one matrix instruction: columns col0 .. col0 + 31 (lane %
 // 32), t0 + 8 * (lane / 32) .. + 7.
+template <int kCols>
 __device__ __forceinline__ bf16x8 read_operand(const char* tile, int t0, int col0, int lane)
 {
     const int t = t0 + lane / 32 * 8, c = col0 + lane % 32 / 16 * 16;
-    const bf16x4 lo = read_transposed(tile, t, c, lane % 16);
-    const bf16x4 hi = read_transposed(tile, t + 4, c, lane % 16);
+    const bf16x4 lo = read_transposed<kCols>(tile, t, c, lane % 16);
+    const bf16x4 hi = read_transposed<kCols>(tile, t + 4, c, lane % 16);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// An fp32 value as three bf16 parts: the leading eight bits, the next eight,
-// the rest (cut off, not rounded, so each remainder is exact and no part
-// overflows).  A value that is not finite is its own first part.
-__device__ __forceinline__ void split3(float x, uint32_t (&part)[3])
+// Eight fp32 values as three bf16 parts each: the leading eight bits, the next
+// eight, the rest (cut off, not rounded, so each remainder is exact and no
+// part overflows).  A value that is not finite is its own first part: the
+// remainder of an infinity is a NaN, and is set to zero, as a NaN's is, whose
+// quiet bit keeps it one in the upper half.
+__device__ __forceinline__ void split3(const Raw8<false>& raw, u32x4 (&part)[3])
 {
-    const uint32_t bits = __float_as_uint(x);
-    if ((bits & 0x7f800000u) == 0x7f800000u) {
-        part[0] = (bits >> 16) | ((bits & 0x7fffffu) ? 0x40u : 0u);
-        part[1] = part[2] = 0;
-        return;
+    constexpr uint32_t kUpper = 0x07060302;  // the upper halves of two words
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[3][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float x = __builtin_canonicalizef(__uint_as_float(raw.v[i / 2][i % 2 * 2 + h]));
+            w[0][h] = __float_as_uint(x);
+            const float rest = x - __uint_as_float(w[0][h] & 0xffff0000u);
+            w[1][h] = rest == rest ? __float_as_uint(rest) : 0u;
+            const float last = __uint_as_float(w[1][h]) - __uint_as_float(w[1][h] & 0xffff0000u);
+            w[2][h] = __float_as_uint(last);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) part[p][i] = __builtin_amdgcn_perm(w[p][1], w[p][0], kUpper);
     }
-    part[0] = bits >> 16;
-    const float rest = x - __uint_as_float(bits & 0xffff0000u);
-    part[1] = __float_as_uint(rest) >> 16;
-    const float last = rest - __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-    part[2] = __float_as_uint(last) >> 16;
 }
 
 // dw (or partial) value at (n, k).
@@ -148,12 +158,12 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[kI][kJ], const Ta
 }
 
 // One tile of dw over the t of [t_first, t_last): block (tile, split).
-template <bool kDyBf16, bool kDwBf16>
+template <bool kDyBf16, bool kDwBf16, int kTile>
 __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
                                                                 int64_t k_all, int64_t per_split, uint32_t tiles_k,
                                                                 Target to)
 {
-    constexpr int kParts = kDyBf16 ? 1 : 3;
+    constexpr int kParts = kDyBf16 ? 1 : 3, kTileT = kDyBf16 ? kStageBf16 : kStageF32;
     constexpr int kBytes = kTileT * kTile * 2;
     __shared__ __attribute__((aligned(16))) char lds[2][kParts + 1][kBytes];  // parts of dy, then x
     const Tile tile = tile_of(blockIdx.x, gridDim.x, tiles_k);
@@ -161,25 +171,30 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
     const int64_t padded = (k_all + kRun - 1) / kRun * kRun;
     const int64_t t_first = blockIdx.y * per_split;
     const int64_t t_last = min(t_first + per_split, tokens);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int wn = wave / 2 * 64, wk = wave % 2 * 64;
-    f32x16 acc[2][2] = {};
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    constexpr int kI = kTile / 64;  // a wavefront's results: kI x kI of 32 x 32
+    const int wn = wave / 2 * (kTile / 2), wk = wave % 2 * (kTile / 2);
+    f32x16 acc[kI][kI] = {};
 
-    // 512 chunks of eight columns of each operand, two per thread.
-    const int t_own = threadIdx.x / 16, chunk = threadIdx.x % 16;
+    // Chunks of eight columns: a thread has the same one of every kStep-th row.
+    constexpr int kChunks = kTile / 8, kStep = kBlock / kChunks, kOwn = kTileT / kStep;
+    const int t_own = tid / kChunks, chunk = tid % kChunks;
     const int64_t n = n0 + chunk * 8, k = k0 + chunk * 8;
-    Raw8<kDyBf16> raw[2];
-    u32x2 codes[2];
-    uint32_t byte[2];
+    Raw8<kDyBf16> raw[kOwn];
+    u32x2 codes[kOwn];
+    uint32_t byte[kOwn];
     auto load = [&](int64_t t0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t t = t0 + t_own + j * 16;
-            const bool live = t < t_last;
-            raw[j] = load8<kDyBf16>(dy.data, t * dy.stride + n, live ? n_all - n : 0);
+        for (int j = 0; j < kOwn; ++j) {
+            const int64_t t = t0 + t_own + j * kStep;
+            raw[j] = load8<kDyBf16>(dy.data, t * dy.stride + n, t < t_last ? n_all - n : 0);
+        }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int64_t t = t0 + t_own + j * kStep;
             codes[j] = u32x2{0, 0};
             byte[j] = 0;
-            if (live && k < padded) {
+            if (t < t_last && k < padded) {
                 const int64_t u = (t * padded + k) / kUnit;
                 codes[j] = reinterpret_cast<const u32x2*>(x.codes)[u];
                 byte[j] = x.scales[u / 4];
@@ -188,24 +203,16 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
     };
     auto put = [&](int buf) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t at = chunk_at(t_own + j * 16, chunk);
-            if (kDyBf16) {
-                *reinterpret_cast<u32x4*>(lds[buf][0] + at) = raw[j].v[0];
-            } else {
-                float v[kUnit];
-                uint32_t part[kUnit][3];
-                widen<kDyBf16>(raw[j], v);
+        for (int j = 0; j < kOwn; ++j) {
+            const uint32_t at = chunk_at<kTile>(t_own + j * kStep, chunk);
+            u32x4 part[3];
+            if constexpr (kDyBf16) part[0] = raw[j].v[0];
+            else split3(raw[j], part);
 #pragma unroll
-                for (int i = 0; i < kUnit; ++i) split3(v[i], part[i]);
+            for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4*>(lds[buf][p] + at) = part[p];
+        }
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) {
-                    u32x4 w;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = part[2 * i][p] | part[2 * i + 1][p] << 16;
-                    *reinterpret_cast<u32x4*>(lds[buf][p] + at) = w;
-                }
-            }
+        for (int j = 0; j < kOwn; ++j) {
             const float scale = __uint_as_float(byte[j] << 23);
             u32x4 w;
 #pragma unroll
@@ -213,7 +220,7 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
                 w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[j][i], scale, false));
                 w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[j][i], scale, true));
             }
-            *reinterpret_cast<u32x4*>(lds[buf][kParts] + at) = w;
+            *reinterpret_cast<u32x4*>(lds[buf][kParts] + chunk_at<kTile>(t_own + j * kStep, chunk)) = w;
         }
     };
 
@@ -225,16 +232,16 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
     for (int64_t t0 = t_first; t0 < t_last; t0 += kTileT, buf ^= 1) {
 #pragma unroll
         for (int t = 0; t < kTileT; t += 16) {
-            bf16x8 b[2];
+            bf16x8 b[kI];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) b[j] = read_operand(lds[buf][kParts], t, wk + j * kFrag, lane);
+            for (int j = 0; j < kI; ++j) b[j] = read_operand<kTile>(lds[buf][kParts], t, wk + j * kFrag, lane);
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bf16x8 a = read_operand(lds[buf][p], t, wn + i * kFrag, lane);
+                for (int i = 0; i < kI; ++i) {
+                    const bf16x8 a = read_operand<kTile>(lds[buf][p], t, wn + i * kFrag, lane);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < kI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
                 }
             }
         }
@@ -330,7 +337,7 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
 
     // The operands' bytes behind a stage's first row, `row` for each of its tokens and `less` fewer in the last one; the
     // stage behind the split's tokens, and those that follow, reach nothing.
-    const int t_count = static_cast<int>(t_last - t_first);
+    const int t_count = static_cast<int>(max(t_last - t_first, static_cast<int64_t>(0)));
     const int whole = t_count / kWideT, rest = t_count % kWideT;
     const uint32_t dy_less = static_cast<uint32_t>((dy.stride - n_all + n0) * 2), x_less = static_cast<uint32_t>(k0);
     auto reach = [&](int s, uint32_t row, uint32_t less) {
@@ -498,55 +505,79 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
     store_tile<kDwBf16>(acc, to, n0 + wn, k0 + wk);
 }
 
-// dw = [dw +] the splits' partial sums, in split order.
-template <bool kDwBf16>
+// dw = [dw +] the splits' partial sums, in split order; four values a thread
+// (partial sums are 16-byte aligned where count % 4 == 0, else one by one).
+template <bool kDwBf16, int kWidth>
 __global__ __launch_bounds__(kBlock) void weight_grad_join_kernel(const float* partials, int splits, int64_t count,
                                                                   void* dw, bool accumulate)
 {
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kBlock;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; i < count; i += step) {
-        float sum = 0.0f;
-        for (int s = 0; s < splits; ++s) sum += partials[s * count + i];
-        store_dw<kDwBf16>(dw, i, sum, accumulate);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kBlock * kWidth;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * kWidth; i < count; i += step) {
+        float sum[kWidth] = {};
+#pragma unroll 8
+        for (int s = 0; s < splits; ++s) {
+            const float* p = partials + s * count + i;
+            if (kWidth == 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+                for (int j = 0; j < kWidth; ++j) sum[j] += v[j];
+            } else {
+                sum[0] += *p;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kWidth; ++j) store_dw<kDwBf16>(dw, i + j, sum[j], accumulate);
     }
 }
 
-struct Shape {
+// A tile's edge, its stage, and two measured times of a stage of it (us): on a
+// CU of its own, and per block where several share a CU.
+struct TileKind {
+    int edge, stage_t;
+    double alone_us, shared_us;
+};
+constexpr TileKind kWide = {kWideTile, kWideT, 1.6, 1.6};  // one block fills a CU
+constexpr TileKind kMid[2] = {{128, kStageF32, 1.14, 0.84}, {128, kStageBf16, 1.0, 0.70}};  // [bf16]
+constexpr TileKind kSmall[2] = {{64, kStageF32, 0.60, 0.30}, {64, kStageBf16, 0.54, 0.29}};
+
+struct Plan {
+    int edge = 0;  // of the tile
     int64_t tiles_n, tiles_k, per_split;
     int splits;
 };
 
-// How the tokens are split: the count of splits under which the slowest CU
-// has least to do, in stages of the tile (`per_cu` blocks run on a CU at
-// once), against the partial sums' way to memory and back.  `stage_us` is a
-// stage's measured time.
-Shape shape_of(int64_t tokens, int64_t n, int64_t k, int tile, int stage_t, int per_cu, double stage_us)
+// The tile and the count of splits of the tokens under which the work should
+// take least: the busiest CU's stages, and with splits the partial sums' way
+// to memory and back (4 TB/s) and their join.  With each choice forced (us):
+// 8192 x 4096 x 4096 bf16 207 wide, 358 at 128, 585 at 64; 2048 x 4096 x 1024
+// 40, 36, 40; 1000 x 1000 x 1000 19.7, 16.3 and 10.8; fp32 777 x 1000 x 2051 31
+// and 26.5, 8192 x 4096 x 4096 860 and 1222.
+Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
 {
-    Shape s;
-    s.tiles_n = (n + tile - 1) / tile;
-    s.tiles_k = (k + tile - 1) / tile;
-    const int64_t tiles = s.tiles_n * s.tiles_k;
-    const int64_t stages = (tokens + stage_t - 1) / stage_t;
-    const int64_t slots = 256 * per_cu;
-    const double join_us = 3.0 + static_cast<double>(n) * k * 8.0 / 4.0e6;  // per split: written and read at 4 TB/s
-    int64_t best = 1;
+    Plan best;
     double least = 0.0;
-    for (int64_t c = 1; c <= 32 && (c == 1 || c * 4 <= stages); ++c) {
-        const int64_t rounds = (tiles * c + slots - 1) / slots;
-        const double cost = rounds * ((stages + c - 1) / c + 4) * stage_us + (c > 1 ? 3.0 + c * (join_us - 3.0) : 0.0);
-        if (c == 1 || cost < least) {
-            best = c;
-            least = cost;
+    const double values = static_cast<double>(n) * static_cast<double>(k);
+    for (const TileKind& kind : {kSmall[bf16], kMid[bf16], kWide}) {
+        if (kind.edge == kWideTile && !wide) continue;
+        const int64_t tiles_n = (n + kind.edge - 1) / kind.edge, tiles_k = (k + kind.edge - 1) / kind.edge;
+        const int64_t stages = (tokens + kind.stage_t - 1) / kind.stage_t;
+        for (int64_t c = 1; c <= 32 && (c == 1 || 2 * c <= stages); ++c) {
+            const int64_t each = (stages + c - 1) / c;
+            const double on_cu = static_cast<double>((tiles_n * tiles_k * c + 255) / 256) * kind.shared_us;
+            const double cost = static_cast<double>(each) * (on_cu > kind.alone_us ? on_cu : kind.alone_us) +
+                                (c > 1 ? 3.0 + (2.0 * static_cast<double>(c) + 1.0) * values * 4.0 / 4.0e6 : 0.0);
+            if (best.edge == 0 || cost < least) {
+                least = cost;
+                best.edge = kind.edge;
+                best.tiles_n = tiles_n;
+                best.tiles_k = tiles_k;
+                best.per_split = each * kind.stage_t;
+                best.splits = static_cast<int>(each > 0 ? (stages + each - 1) / each : 1);
+            }
         }
     }
-    const int64_t per = (stages + best - 1) / best;
-    s.per_split = per * stage_t;
-    s.splits = static_cast<int>(per > 0 ? (stages + per - 1) / per : 1);
-    return s;
+    return best;
 }
-
-Shape narrow_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kTile, kTileT, 2, 1.2); }
-Shape wide_shape(int64_t tokens, int64_t n, int64_t k) { return shape_of(tokens, n, k, kWideTile, kWideT, 1, 1.6); }
 
 // Whether dy's rows are whole 16-byte chunks.
 bool chunk_rows(const Matrix& dy, int64_t n)
@@ -556,32 +587,35 @@ bool chunk_rows(const Matrix& dy, int64_t n)
 
 // The wide tile takes bf16 gradients of rows that keep two stages' offsets
 // below 2^32 bytes.
-bool wide_fits(const Matrix& dy, bool dy_bf16, int64_t tokens, int64_t n, int64_t k)
+bool wide_fits(int64_t dy_stride, bool dy_bf16, int64_t n, int64_t k)
 {
-    return dy_bf16 && dy.stride < 1 << 23 && k <= 1 << 25 && tokens >= 256 && n * k >= 1 << 20;
+    return dy_bf16 && dy_stride < 1 << 23 && n >= 64 && k >= 64 && k <= 1 << 25;
 }
 
-size_t scratch_of(const Shape& s, int64_t n, int64_t k)
+size_t scratch_of(const Plan& s, int64_t n, int64_t k)
 {
     return s.splits > 1 ? static_cast<size_t>(s.splits) * n * k * sizeof(float) : 0;
 }
 
 }  // namespace
 
-// Whichever tile the gradient's layout will allow.
+// Whichever plan the gradient's type and stride will give.
 size_t weight_grad_scratch(int64_t tokens, int64_t out_features, int64_t in_features)
 {
-    const size_t narrow = scratch_of(narrow_shape(tokens, out_features, in_features), out_features, in_features);
-    const size_t wide = scratch_of(wide_shape(tokens, out_features, in_features), out_features, in_features);
-    return narrow > wide ? narrow : wide;
+    size_t most = 0;
+    for (int i = 0; i < 3; ++i) {  // fp32; bf16 without and with the wide tile
+        const bool wide = i == 2 && wide_fits(out_features, true, out_features, in_features);
+        const size_t need = scratch_of(plan_of(tokens, out_features, in_features, i > 0, wide), out_features, in_features);
+        if (need > most) most = need;
+    }
+    return most;
 }
 
 hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tokens, int64_t out_features,
                                    int64_t in_features, void* dw, bool dw_bf16, bool accumulate, void* scratch,
                                    hipStream_t stream)
 {
-    const bool wide = wide_fits(dy, dy_bf16, tokens, out_features, in_features);
-    const Shape s = wide ? wide_shape(tokens, out_features, in_features) : narrow_shape(tokens, out_features, in_features);
+    const Plan s = plan_of(tokens, out_features, in_features, dy_bf16, wide_fits(dy.stride, dy_bf16, out_features, in_features));
     float* partials = s.splits > 1 ? static_cast<float*>(scratch) : nullptr;
     const dim3 grid(static_cast<uint32_t>(s.tiles_n * s.tiles_k), s.splits);
     const uint32_t tk = static_cast<uint32_t>(s.tiles_k);
@@ -589,26 +623,45 @@ hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tok
         kernel<<<grid, kBlock, 0, stream>>>(dy, x, tokens, out_features, in_features, s.per_split, tk,
                                             Target{dw, partials, accumulate, out_features, in_features});
     };
-    if (wide && chunk_rows(dy, out_features)) {
-        if (dw_bf16) run(weight_grad_wide_kernel<true, true>);
-        else run(weight_grad_wide_kernel<true, false>);
-    } else if (wide) {
-        if (dw_bf16) run(weight_grad_wide_kernel<false, true>);
-        else run(weight_grad_wide_kernel<false, false>);
-    } else if (dy_bf16) {
-        if (dw_bf16) run(weight_grad_kernel<true, true>);
-        else run(weight_grad_kernel<true, false>);
+    if (s.edge == kWideTile) {
+        if (chunk_rows(dy, out_features)) {
+            if (dw_bf16) run(weight_grad_wide_kernel<true, true>);
+            else run(weight_grad_wide_kernel<true, false>);
+        } else {
+            if (dw_bf16) run(weight_grad_wide_kernel<false, true>);
+            else run(weight_grad_wide_kernel<false, false>);
+        }
+    } else if (s.edge == 128) {
+        if (dy_bf16) {
+            if (dw_bf16) run(weight_grad_kernel<true, true, 128>);
+            else run(weight_grad_kernel<true, false, 128>);
+        } else {
+            if (dw_bf16) run(weight_grad_kernel<false, true, 128>);
+            else run(weight_grad_kernel<false, false, 128>);
+        }
     } else {
-        if (dw_bf16) run(weight_grad_kernel<false, true>);
-        else run(weight_grad_kernel<false, false>);
+        if (dy_bf16) {
+            if (dw_bf16) run(weight_grad_kernel<true, true, 64>);
+            else run(weight_grad_kernel<true, false, 64>);
+        } else {
+            if (dw_bf16) run(weight_grad_kernel<false, true, 64>);
+            else run(weight_grad_kernel<false, false, 64>);
+        }
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !partials) return e;
     const int64_t count = out_features * in_features;
-    const int64_t blocks = (count + kBlock - 1) / kBlock;
-    const int join_grid = static_cast<int>(blocks < 2048 ? blocks : 2048);
-    if (dw_bf16) weight_grad_join_kernel<true><<<join_grid, kBlock, 0, stream>>>(partials, s.splits, count, dw, accumulate);
-    else weight_grad_join_kernel<false><<<join_grid, kBlock, 0, stream>>>(partials, s.splits, count, dw, accumulate);
+    const int width = count % 4 == 0 ? 4 : 1;
+    const int64_t blocks = (count + kBlock * width - 1) / (kBlock * width);
+    const int join_grid = static_cast<int>(blocks < 1 << 20 ? blocks : 1 << 20);
+    auto join = [&](auto kernel) { kernel<<<join_grid, kBlock, 0, stream>>>(partials, s.splits, count, dw, accumulate); };
+    if (width == 4) {
+        if (dw_bf16) join(weight_grad_join_kernel<true, 4>);
+        else join(weight_grad_join_kernel<false, 4>);
+    } else {
+        if (dw_bf16) join(weight_grad_join_kernel<true, 1>);
+        else join(weight_grad_join_kernel<false, 1>);
+    }
     return hipGetLastError();
 }
 

@@ -14,9 +14,9 @@ using mps::fail;
 using mps::ok;
 
 constexpr int64_t kMostRows = (1ll << 31) - 1;
-constexpr int64_t kMostCols = 1ll << 28;
+constexpr int64_t kMostCols = 1ll << 27;
 constexpr int64_t kMostStride = (1ll << 31) - 1;
-constexpr int64_t kMostTiles = 1ll << 23;  // of 128 x 128 values of a weight gradient
+constexpr int64_t kMostTiles = 1ll << 21;  // of 128 x 128 values of a weight gradient
 constexpr size_t kWorkspaceAlign = 256;
 
 int elem_bytes(mps_dtype t) { return t == MPS_DTYPE_BF16 ? 2 : 4; }
@@ -33,7 +33,7 @@ int check_shape(int64_t rows, int64_t cols, const char* rows_name, const char* c
         return fail(MPS_ERR_INVALID_ARGUMENT, "%s = %lld: 0 to 2^31 - 1", rows_name, static_cast<long long>(rows));
     }
     if (cols < 1 || cols > kMostCols) {
-        return fail(MPS_ERR_INVALID_ARGUMENT, "%s = %lld: 1 to 2^28", cols_name, static_cast<long long>(cols));
+        return fail(MPS_ERR_INVALID_ARGUMENT, "%s = %lld: 1 to 2^27", cols_name, static_cast<long long>(cols));
     }
     return MPS_OK;
 }
@@ -163,7 +163,7 @@ int weight_grad_shape(int64_t tokens, int64_t out_features, int64_t in_features)
     if (!rc) rc = check_shape(tokens, in_features, "tokens", "in_features");
     if (rc) return rc;
     if (((out_features + 127) / 128) * ((in_features + 127) / 128) > kMostTiles) {
-        return fail(MPS_ERR_INVALID_ARGUMENT, "a weight gradient of more than 2^23 tiles of 128 x 128");
+        return fail(MPS_ERR_INVALID_ARGUMENT, "a weight gradient of more than 2^21 tiles of 128 x 128");
     }
     return MPS_OK;
 }

@@ -90,7 +90,7 @@ def test_keep_and_read_back(oracle_lib, dtype, rows, cols):
     for out_type in TYPES:
         out, whole = framed(rows, cols, out_type)
         mps.act8_load(codes, scales, out)
-        assert torch.equal(out.cpu(), want.to(torch.float32).to(out_type))
+        assert torch.equal(out, want.to(torch.float32).to(out_type))
         check_frames(whole, rows, cols)
 
 
@@ -104,7 +104,7 @@ def test_nonfinite_runs(oracle_lib, dtype):
     mps.act8_save(x, codes, scales)
     check_kept(codes, scales, ref.keep(oracle_lib, x))
     back = mps.act8_load(codes, scales, torch.empty(6, 130, dtype=torch.float32, device=DEV))
-    want = ref.values(codes, scales, 130).float()
+    want = ref.values(codes, scales, 130).float().cpu()
     assert torch.equal(torch.isnan(back.cpu()), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(back.cpu(), nan=1.0), torch.nan_to_num(want, nan=1.0))
     assert torch.isnan(back[0, :32]).all() and not torch.isnan(back[0, 32:]).any()
@@ -199,7 +199,7 @@ def test_rmsnorm_backward(oracle_lib, dtype, rows, cols, full):
     near(dweight[:cols], want_dw, size * (rows + 1030) * U + 1e-45, "dweight")
     if full and rows:
         # The same two fp32 products as the bytes are made from: bitwise.
-        again = xk.float().cpu() * rstd.cpu()[:, None] * w.cpu()
+        again = xk.float() * rstd[:, None] * w
         check_kept(out[0], out[1], ref.keep(oracle_lib, again), out[2], out[3])
 
 

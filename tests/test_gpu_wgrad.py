@@ -18,12 +18,23 @@ TYPES = [torch.bfloat16, torch.float32]
 SHAPES = [(1, 1, 1), (5, 3, 7), (31, 33, 32), (32, 128, 128), (33, 129, 131), (64, 64, 256), (65, 256, 96), (0, 40, 50),
           (100, 8, 2051), (257, 513, 40), (515, 1000, 33), (1030, 260, 520), (2500, 72, 136), (4099, 16, 24), (300, 512, 768),
           (700, 768, 512),
-          # from here on bf16 gradients take tiles of 256 (where their rows allow it), with edges in every direction
-          (256, 1024, 1024), (257, 1032, 1025), (1030, 520, 2051), (319, 2056, 520), (1500, 264, 4000), (400, 1025, 1030)]
+          (257, 1032, 1025), (1030, 520, 2051), (1500, 264, 4000), (12000, 260, 300),
+          # tiles of 128, without and with splits of the tokens
+          (2048, 2048, 2048), (3000, 1025, 2050),
+          # bf16 gradients: tiles of 256, with splits and without, rows of whole 16-byte chunks and odd ones
+          (4000, 1032, 2056), (4000, 1031, 2056), (600, 4096, 4352), (700, 4099, 4100)]
 
 
 def gen(seed):
     return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def kept(oracle_lib, x):
+    """x in 8 bits: by the oracle, or, where that would take seconds, by act8_save
+    (which is compared with the oracle bitwise in its own tests)."""
+    if x.numel() < 300000:
+        return tuple(v.to(DEV) for v in ref.keep(oracle_lib, x))
+    return mps.act8_save(x.to(DEV), *mps.act8_empty(*x.shape, DEV))
 
 
 def workspace(t, n, k):
@@ -53,7 +64,7 @@ def check_guard(buf, n, k, offset=1):
 def test_whole_numbers_bitwise(oracle_lib, dtype, dw_type, t, n, k):
     g = gen(t + 3 * n + 7 * k)
     x = torch.randint(-4, 5, (t, k), generator=g, device=DEV).float()
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, x))
+    codes, scales = kept(oracle_lib, x)
     codes[:, k:] = 0x38
     # A matrix inside a larger one: 16-byte rows where n allows them, else an odd start and stride.
     left = 8 if n % 8 == 0 else 3
@@ -78,7 +89,7 @@ def test_whole_numbers_bitwise(oracle_lib, dtype, dw_type, t, n, k):
 @pytest.mark.parametrize("t,n,k", SHAPES + [(3000, 384, 640), (8200, 130, 70)])
 def test_values(oracle_lib, dtype, t, n, k):
     g = gen(5 * t + n + k)
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, torch.randn(t, k, generator=g, device=DEV)))
+    codes, scales = kept(oracle_lib, torch.randn(t, k, generator=g, device=DEV))
     dy = (torch.randn(t, n, generator=g, device=DEV) * 0.01).to(dtype)
     want, size = product(dy, codes, scales, k)
     dw = torch.empty(n, k, device=DEV)
@@ -93,20 +104,20 @@ def test_fp32_gradients_keep_all_their_bits(oracle_lib):
     """One token and x = 1: dw is dy itself, every bit of it."""
     dy = torch.randn(1, 400, device=DEV)
     dy[0, :6] = torch.tensor([3.4028234e38, -3.4028234e38, 1.1754944e-38, 1.0000001, -0.99999994, 0.0])
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, torch.ones(1, 32)))
+    codes, scales = kept(oracle_lib, torch.ones(1, 32))
     dw = torch.empty(400, 32, device=DEV)
     mps.act8_weight_grad(dy, codes, scales, dw, workspace(1, 400, 32))
     assert torch.equal(dw, dy.t().expand(400, 32))
 
 
 @pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 70, 150, 160), (torch.float32, 70, 150, 160),
-                                         (torch.bfloat16, 270, 1032, 1100)])
+                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 700, 4099, 4100)])
 def test_nonfinite_values_stay_in_their_rows_and_columns(oracle_lib, dtype, t, n, k):
     x = torch.ones(t, k)
     x[3, 40] = float("nan")  # the run of columns 32 .. 63
     dy = torch.ones(t, n, device=DEV, dtype=dtype)
     dy[5, 7], dy[6, 8], dy[9, 9] = float("inf"), -float("inf"), float("nan")
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, x))
+    codes, scales = kept(oracle_lib, x)
     dw = mps.act8_weight_grad(dy, codes, scales, torch.empty(n, k, device=DEV), workspace(t, n, k))
     clean_rows = [i for i in range(n) if i not in (7, 8, 9)]
     clean = torch.ones(k, dtype=torch.bool)
@@ -121,7 +132,7 @@ def test_small_and_large_kept_values(oracle_lib):
     exact where bf16 holds the value."""
     e = torch.arange(-126, 100, dtype=torch.float32)
     x = torch.exp2(e)[:, None].expand(-1, 32).contiguous()
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, x))
+    codes, scales = kept(oracle_lib, x)
     t = x.shape[0]
     dy = torch.zeros(t, t, device=DEV, dtype=torch.bfloat16)
     dy[torch.arange(t), torch.arange(t)] = 2.0
@@ -129,10 +140,10 @@ def test_small_and_large_kept_values(oracle_lib):
     assert torch.equal(dw.cpu(), x * 2)
 
 
-@pytest.mark.parametrize("t,n,k", [(5000, 300, 200), (5000, 1024, 1040)])
+@pytest.mark.parametrize("t,n,k", [(5000, 300, 200), (5000, 1024, 1040), (16384, 1024, 1024)])
 def test_two_runs_give_the_same_bits(oracle_lib, t, n, k):
     g = gen(9)
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, torch.randn(t, k, generator=g, device=DEV)))
+    codes, scales = kept(oracle_lib, torch.randn(t, k, generator=g, device=DEV))
     dy = torch.randn(t, n, generator=g, device=DEV).to(torch.bfloat16)
     ws = workspace(t, n, k)
     runs = []
@@ -143,7 +154,7 @@ def test_two_runs_give_the_same_bits(oracle_lib, t, n, k):
 
 
 @pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 40, 64, 64), (torch.float32, 40, 64, 64),
-                                         (torch.bfloat16, 400, 1024, 1024), (torch.bfloat16, 257, 1024, 1024)])
+                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 257, 1024, 1024)])
 def test_offsets_past_32_bits(oracle_lib, dtype, t, n, k):
     """dy with more than 2^32 elements: a stride that puts the last tokens far out
     (in steps of less and of more than 2^25 elements)."""
@@ -156,7 +167,7 @@ def test_offsets_past_32_bits(oracle_lib, dtype, t, n, k):
     dy = big.as_strided((t, n), (stride, 1))
     dy.copy_(small)
     x = torch.randint(-4, 5, (t, k), generator=g, device=DEV).float()
-    codes, scales = (v.to(DEV) for v in ref.keep(oracle_lib, x))
+    codes, scales = kept(oracle_lib, x)
     dw = mps.act8_weight_grad(dy, codes, scales, torch.empty(n, k, device=DEV), workspace(t, n, k))
     assert torch.equal(dw, product(small, codes, scales, k)[0].float())
 

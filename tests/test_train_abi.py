@@ -97,7 +97,7 @@ def test_sizes(lib):
     # a gradient as large as the chip's tiles is not split
     assert mps.act8_weight_grad_workspace_bytes(16384, 14336, 4096) == 0
     assert mps.act8_weight_grad_workspace_bytes(16384, 512, 512) > 0
-    for bad in ((-1, 8), (1 << 31, 8), (8, 0), (8, (1 << 28) + 1)):
+    for bad in ((-1, 8), (1 << 31, 8), (8, 0), (8, (1 << 27) + 1)):
         with pytest.raises(mps.MpsError) as e:
             mps.policy_loss_workspace_bytes(*bad)
         assert e.value.code == -22

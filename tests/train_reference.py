@@ -30,16 +30,15 @@ def keep(oracle_lib, x: torch.Tensor):
 
 
 def values(codes: torch.Tensor, scales: torch.Tensor, cols: int) -> torch.Tensor:
-    """float64 values of codes and scales, decoded bit by bit."""
-    c = codes.cpu().numpy().astype(np.int64)
-    s = scales.cpu().numpy().astype(np.float64)
-    sign = np.where(c & 0x80, -1.0, 1.0)
-    e, m = (c >> 3) & 15, (c & 7).astype(np.float64)
-    v = np.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * np.exp2(e - 7.0))
-    v = np.where((c & 0x7f) == 0x7f, np.nan, sign * v)
-    b = np.repeat(s, RUN, axis=1)
-    out = np.where(b == 255, np.nan, v * np.exp2(b - 127))
-    return torch.from_numpy(out[:, :cols])
+    """float64 values of codes and scales, decoded bit by bit, on their device."""
+    b = torch.arange(256, dtype=torch.float64)
+    e, m = ((b % 128) / 8).floor(), b % 8
+    table = torch.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * torch.exp2(e - 7.0)) * torch.where(b >= 128, -1.0, 1.0)
+    table[127], table[255] = float("nan"), float("nan")
+    scale = torch.exp2(b - 127)
+    scale[255] = float("nan")
+    v = table.to(codes.device)[codes.long()] * scale.to(codes.device)[scales.long()].repeat_interleave(RUN, 1)
+    return v[:, :cols]
 
 
 def rmsnorm(x, weight, eps):
