@@ -25,17 +25,44 @@ __device__ __forceinline__ float exp_below(float x, float top) { return __builti
 
 // A share of a row: its largest logit and the sum of e^(x - top).  An empty
 // share, or one of -inf logits only, is {-inf, 0}; a NaN or +inf logit makes
-// the sum NaN.
+// the sum NaN.  (e is 2^kLog2e throughout, 1 + 1.3e-8 times as steep as the
+// real one; row_values() measures the label's logit in the same units, so that
+// only 1.3e-8 of its distance from the row's mean remains.)
 struct Share {
     float top;
     double sum;
 };
 
-__device__ __forceinline__ Share join(const Share& a, const Share& b)
+// The share of a wavefront, from its lanes' tops and sums; every lane gets it.
+__device__ __forceinline__ Share wave_share(float top, float sum)
 {
-    const float top = fmaxf(a.top, b.top);
+    float most = top;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
+    const float base = most == -INFINITY ? 0.0f : most;
+    return {most, wave_sum(static_cast<double>(sum * exp_below(top, base)))};
+}
+
+// The sum of a share under a larger top: in fp64, since few factors decide a
+// row's sum here (in fp32 their errors, 1e-7 each, showed in the loss).
+__device__ __forceinline__ double rescaled(const Share& s, float top)
+{
     const float base = top == -INFINITY ? 0.0f : top;
-    return {top, a.sum * static_cast<double>(exp_below(a.top, base)) + b.sum * static_cast<double>(exp_below(b.top, base))};
+    return s.sum * exp2((static_cast<double>(s.top) - static_cast<double>(base)) * static_cast<double>(kLog2e));
+}
+
+// Joins the shares of each group of kLanes lanes (a power of two), in a fixed
+// order; every lane of the group gets the result.
+template <int kLanes>
+__device__ __forceinline__ Share lanes_join(const Share& s)
+{
+    float top = s.top;
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+    double sum = rescaled(s, top);
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor(sum, off, kWave);
+    return {top, sum};
 }
 
 // What one row gives to the loss, and the two factors of its gradient,
@@ -55,7 +82,8 @@ __device__ __attribute__((noinline)) RowResult row_values(float top, double sum,
     if (top == -INFINITY && sum == 0.0) return r;  // nothing to choose from: left out
     r.top = top;
     r.label_logit = label_logit;
-    const double logp = static_cast<double>(label_logit) - static_cast<double>(top) - log(sum);
+    constexpr double kSteep = static_cast<double>(kLog2e) * 0.69314718055994530942;  // 1 + 1.3e-8 less
+    const double logp = (static_cast<double>(label_logit) - static_cast<double>(top)) * kSteep - log(sum);
     r.logp = static_cast<float>(logp);
     if (!loss_too) return r;
     const double w = weight, adv = advantage;
@@ -124,20 +152,6 @@ __device__ __forceinline__ RowResult finish_row(const PolicyArgs& a, int64_t row
     return r;
 }
 
-// Joins the shares of the first `n` (a power of two) lanes of each group of
-// n, in a fixed order; every lane of the group gets the result.
-template <int kLanes>
-__device__ __forceinline__ Share lanes_join(Share s)
-{
-    const int lane = threadIdx.x % kWave;
-#pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) {
-        const Share o = {__shfl_xor(s.top, off, kWave), __shfl_xor(s.sum, off, kWave)};
-        s = (lane & off) ? join(o, s) : join(s, o);
-    }
-    return s;
-}
-
 constexpr int kDeep = 4;  // units of eight logits that a thread has under way
 
 // A thread's running largest logit, and the sum under it.
@@ -156,6 +170,13 @@ struct Running {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) x[i] = exp_below(x[i], under);
         sum = before + (((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+    }
+
+    __device__ __forceinline__ void take(float x)
+    {
+        const float now = fmaxf(top, x), under = now == -INFINITY ? 0.0f : now;
+        sum = sum * exp_below(top, under) + exp_below(x, under);
+        top = now;
     }
 };
 
@@ -223,8 +244,9 @@ __device__ __forceinline__ void forget(Raw8<kBf16>& r)
     for (int i = 0; i < (kBf16 ? 1 : 2); ++i) asm volatile("" : "+v"(r.v[i]));
 }
 
-// The share of thread `t` of kTeam in the logits [first, last) of a row, both
-// in whole units except that `last` may be the row's end.
+// Reads thread t's part (of kTeam threads) of the logits [first, last) of a
+// row, both in whole units except that `last` may be the row's end; the share
+// of its whole wavefront.
 template <bool kBf16, int kTeam>
 __device__ __forceinline__ Share read_share(const PolicyArgs& a, int64_t row, int64_t first, int64_t last, int t)
 {
@@ -240,12 +262,8 @@ __device__ __forceinline__ Share read_share(const PolicyArgs& a, int64_t row, in
         for (int v = 0; v < kDeep; ++v) run.take(raw[v]);
     }
     for (; u < full; u += kTeam) run.take(in.load(u));
-    Share s = {run.top, static_cast<double>(run.sum)};
-    if (t < static_cast<int>(count % kUnit)) {
-        const float x = logit_at(a, kBf16, row * a.logits.stride + first + full * kUnit + t);
-        s = join(s, {x, x == -INFINITY ? 0.0 : static_cast<double>(exp_below(x, x))});
-    }
-    return s;
+    if (t < static_cast<int>(count % kUnit)) run.take(logit_at(a, kBf16, row * a.logits.stride + first + full * kUnit + t));
+    return wave_share(run.top, run.sum);
 }
 
 // The gradient of the logits [first, last) of a row, by thread t of kTeam;
@@ -287,7 +305,7 @@ __device__ __forceinline__ void write_gradient(const PolicyArgs& a, int64_t row,
 
 // ------------------------------------------------------ a row per block ---
 
-// The shares of a block's wavefronts, joined and finished by the first one;
+// The wavefronts' shares of a block, joined and finished by the first one;
 // the result is in `result` behind the barrier.  Called by every thread.
 template <bool kBf16, int kThreads>
 __device__ __forceinline__ void finish_block(const PolicyArgs& a, int64_t row, bool live, Share mine, Share* shares,
@@ -295,10 +313,7 @@ __device__ __forceinline__ void finish_block(const PolicyArgs& a, int64_t row, b
 {
     constexpr int kWaves = kThreads / kWave;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    if (live) {
-        mine = lanes_join<kWave>(mine);
-        if (lane == 0) shares[wave] = mine;
-    }
+    if (live && lane == 0) shares[wave] = mine;
     __syncthreads();
     if (wave == 0) {
         const Share s = lanes_join<kWaves>(shares[lane % kWaves]);
@@ -372,11 +387,8 @@ __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, dou
                 }
             }
             for (uint32_t u = t + (kRegs + kLds) * kThreads; u < full; u += kThreads) run.take(in.load(u));
-            s = {run.top, static_cast<double>(run.sum)};
-            if (t < rest) {
-                const float x = logit_at(a, kBf16, row * a.logits.stride + full * kUnit + t);
-                s = join(s, {x, x == -INFINITY ? 0.0 : static_cast<double>(exp_below(x, x))});
-            }
+            if (t < rest) run.take(logit_at(a, kBf16, row * a.logits.stride + full * kUnit + t));
+            s = wave_share(run.top, run.sum);
         }
         finish_block<kBf16, kThreads>(a, row, live, s, shares, &result, total);
         const int64_t next = row + gridDim.x;
@@ -434,7 +446,7 @@ __global__ __launch_bounds__(kBlock) void policy_wave_kernel(PolicyArgs a, doubl
         const int n = static_cast<int>(min(static_cast<int64_t>(kGroup), a.rows - first));
         for (int i = wave; i < n; i += kWavesPerBlock) {
             if (!row_live(a, first + i)) continue;
-            const Share s = lanes_join<kWave>(read_share<kBf16, kWave>(a, first + i, 0, a.vocab, lane));
+            const Share s = read_share<kBf16, kWave>(a, first + i, 0, a.vocab, lane);
             if (lane == 0) shares[i] = s;
         }
         __syncthreads();
@@ -479,7 +491,7 @@ __global__ __launch_bounds__(kBlock) void policy_shares_kernel(PolicyArgs a, int
     const int64_t row = blockIdx.x;
     if (!row_live(a, row)) return;
     if (blockIdx.y == 0 && threadIdx.x == 0) label_logits[row] = label_logit_of(a, kBf16, row);
-    Share s = lanes_join<kWave>(read_share<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x));
+    Share s = read_share<kBf16, kBlock>(a, row, span.first, span.last, threadIdx.x);
     if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
     __syncthreads();
     if (threadIdx.x < kWave) {
@@ -510,8 +522,9 @@ __global__ __launch_bounds__(kBlock) void policy_rows_kernel(PolicyArgs a, int s
     } else if (wave == 1 && a.loss && blockIdx.x == 0 && blockIdx.y == 0) {
         double loss = 0.0;
         if (lane < a.rows && row_live(a, lane)) {
-            Share s = in[lane * shares];
-            for (int i = 1; i < shares; ++i) s = join(s, in[lane * shares + i]);
+            Share s = {-INFINITY, 0.0};
+            for (int i = 0; i < shares; ++i) s.top = fmaxf(s.top, in[lane * shares + i].top);
+            for (int i = 0; i < shares; ++i) s.sum += rescaled(in[lane * shares + i], s.top);
             PolicyArgs mine = a;
             mine.token_logp = mine.token_kl = nullptr;
             loss = finish_row(mine, lane, true, s, label_logits[lane]).loss;
