@@ -62,23 +62,24 @@ def _function(name: str):
     return _functions[name]
 
 
-# The current stream's handle without building a Stream object, where torch
-# offers it (a call's checks cost the host about as much as its launch).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# A call's checks cost the host about as much as its launch, so they are kept
+# short: a device is its index, and the current device and stream come without
+# building Python objects where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _enqueue(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+def _enqueue(name: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> None:
     """Call an entry point on `stream` with the tensors' device current."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream: of {stream.device}, with tensors on {device}")
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(device.index)
+    if stream is None:
+        handle = _raw_stream(device)
     else:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        if stream.device.index != device:
+            raise ValueError(f"stream: of {stream.device}, with tensors on cuda:{device}")
+        handle = stream.cuda_stream
     f = _functions[name] if _bound is binding._lib and _bound is not None else _function(name)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device:
         rc = f(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -88,8 +89,8 @@ def _enqueue(name: str, device: torch.device, stream: Optional[torch.cuda.Stream
 
 
 def _matrix(t: torch.Tensor, name: str):
-    """(C dtype, rows, cols, row stride) of the matrix that fixes a call's type,
-    shape and device."""
+    """(C dtype, rows, cols, row stride, device) of the matrix that fixes a call's
+    type, shape and device."""
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: a matrix, got {len(shape)} dimensions")
@@ -102,7 +103,8 @@ def _matrix(t: torch.Tensor, name: str):
         kind = MPS_DTYPE_F32
     else:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {dtype}")
-    return kind, shape[0], shape[1], _row_stride(t, shape[0], shape[1], name)
+    rows, cols = shape
+    return kind, rows, cols, _row_stride(t, rows, cols, name), t.get_device()
 
 
 def _row_stride(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
@@ -116,37 +118,37 @@ def _rows(t: torch.Tensor, like: torch.Tensor, shape, name: str) -> int:
     """The row stride of a matrix of `like`'s type and device."""
     if t.dtype is not like.dtype:
         raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
+    if t.device != like.device:
         raise ValueError(f"{name}: must be on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
     return _row_stride(t, shape[0], shape[1], name)
 
 
-def _flat(t: torch.Tensor, dtype, shape, device, name: str) -> int:
+def _flat(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
     """The address of a contiguous tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be on cuda:{device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
-def _kept(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, device, name: str = ""):
+def _kept(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, device: int, name: str = ""):
     runs = (cols + MPS_Q8_BLOCK - 1) // MPS_Q8_BLOCK
     return (_flat(codes, torch.uint8, (rows, runs * MPS_Q8_BLOCK), device, name + "codes"),
             _flat(scales, torch.uint8, (rows, runs), device, name + "scales"))
 
 
-def _workspace(t: Optional[torch.Tensor], device):
+def _workspace(t: Optional[torch.Tensor], device: int):
     if t is None:
         return None, 0
-    if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace: contiguous uint8 tensor on {device}")
+    if t.dtype is not torch.uint8 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace: contiguous uint8 tensor on cuda:{device}")
     return t.data_ptr(), t.numel()
 
 
@@ -167,8 +169,7 @@ def act8_empty(rows: int, cols: int, device) -> tuple:
 def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """Keep the matrix x in 8 bits; returns (codes, scales)."""
-    kind, rows, cols, stride = _matrix(x, "x")
-    dev = x.device
+    kind, rows, cols, stride, dev = _matrix(x, "x")
     _enqueue("act8_save", dev, stream, x.data_ptr(), kind, stride, rows, cols,
              *_kept(codes, scales, rows, cols, dev))
     return codes, scales
@@ -177,8 +178,7 @@ def act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
 def act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The values that codes and scales stand for, in out's type."""
-    kind, rows, cols, stride = _matrix(out, "out")
-    dev = out.device
+    kind, rows, cols, stride, dev = _matrix(out, "out")
     _enqueue("act8_load", dev, stream, *_kept(codes, scales, rows, cols, dev), rows, cols,
              out.data_ptr(), kind, stride)
     return out
@@ -189,8 +189,7 @@ def act8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: torch.T
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out = x * rstd * weight per row, rstd = 1 / sqrt(mean(x^2) + eps) (float32,
     one per row); x is kept in codes and scales.  weight: float32."""
-    kind, rows, cols, stride = _matrix(x, "x")
-    dev = x.device
+    kind, rows, cols, stride, dev = _matrix(x, "x")
     _enqueue("act8_rmsnorm", dev, stream, x.data_ptr(), kind, stride, rows, cols,
              _flat(weight, torch.float32, (cols,), dev, "weight"), float(eps), out.data_ptr(),
              _rows(out, x, x.shape, "out"), _flat(rstd, torch.float32, (rows,), dev, "rstd"),
@@ -212,8 +211,7 @@ def act8_rmsnorm_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.T
     """dx and dweight (float32; added to with accumulate) of act8_rmsnorm from dy
     and the kept x and rstd; dx gets residual_grad added, and out_codes and
     out_scales, if given, the norm's output again in 8 bits."""
-    kind, rows, cols, stride = _matrix(dy, "dy")
-    dev = dy.device
+    kind, rows, cols, stride, dev = _matrix(dy, "dy")
     if (out_codes is None) != (out_scales is None):
         raise ValueError("out_codes and out_scales: both or neither")
     res = (None, 0) if residual_grad is None else (residual_grad.data_ptr(),
@@ -231,8 +229,7 @@ def act8_swiglu(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor, gate_co
                 gate_scales: torch.Tensor, up_codes: torch.Tensor, up_scales: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out = gate * sigmoid(gate) * up; gate and up are kept in 8 bits."""
-    kind, rows, cols, stride = _matrix(gate, "gate")
-    dev = gate.device
+    kind, rows, cols, stride, dev = _matrix(gate, "gate")
     _enqueue("act8_swiglu", dev, stream, gate.data_ptr(), stride,
              up.data_ptr(), _rows(up, gate, gate.shape, "up"), kind, rows, cols, out.data_ptr(),
              _rows(out, gate, gate.shape, "out"), *_kept(gate_codes, gate_scales, rows, cols, dev, "gate_"),
@@ -247,8 +244,7 @@ def act8_swiglu_backward(dout: torch.Tensor, gate_codes: torch.Tensor, gate_scal
                          stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """(dgate, dup) of act8_swiglu from dout and the kept gate and up; out_codes
     and out_scales, if given, get the forward output again in 8 bits."""
-    kind, rows, cols, stride = _matrix(dout, "dout")
-    dev = dout.device
+    kind, rows, cols, stride, dev = _matrix(dout, "dout")
     if (out_codes is None) != (out_scales is None):
         raise ValueError("out_codes and out_scales: both or neither")
     again = (None, None) if out_codes is None else _kept(out_codes, out_scales, rows, cols, dev, "out_")
@@ -269,9 +265,8 @@ def act8_weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """dw[out_features, in_features] (float32 or bfloat16, contiguous; added to with
     accumulate) = dy^T x, x the kept activation [tokens, in_features]."""
-    kind, tokens, n, stride = _matrix(dy, "dy")
-    dw_kind, _, k, _ = _matrix(dw, "dw")
-    dev = dy.device
+    kind, tokens, n, stride, dev = _matrix(dy, "dy")
+    dw_kind, _, k, _, _ = _matrix(dw, "dw")
     _enqueue("act8_weight_grad", dev, stream, dy.data_ptr(), kind, stride,
              *_kept(codes, scales, tokens, k, dev), tokens, n, k, _flat(dw, dw.dtype, (n, k), dev, "dw"),
              dw_kind, 1 if accumulate else 0, *_workspace(workspace, dev))
@@ -295,8 +290,7 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
     KL term, and with dlogits (logits' type; may be logits itself) the gradient.
     labels: int64; the other vectors float32, one value per row.  Rows with a
     label outside the vocabulary or a weight of 0 are left out."""
-    kind, rows, vocab, stride = _matrix(logits, "logits")
-    dev = logits.device
+    kind, rows, vocab, stride, dev = _matrix(logits, "logits")
 
     def vector(t, name):
         return None if t is None else _flat(t, torch.float32, (rows,), dev, name)
@@ -314,8 +308,7 @@ def token_logprobs(logits: torch.Tensor, labels: torch.Tensor, out: torch.Tensor
                    workspace: Optional[torch.Tensor],
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """out (float32, one per row) = logits[label] - logsumexp(logits)."""
-    kind, rows, vocab, stride = _matrix(logits, "logits")
-    dev = logits.device
+    kind, rows, vocab, stride, dev = _matrix(logits, "logits")
     _enqueue("token_logprobs", dev, stream, logits.data_ptr(), kind,
              stride, rows, vocab,
              _flat(labels, torch.int64, (rows,), dev, "labels"), _flat(out, torch.float32, (rows,), dev, "out"),

@@ -132,12 +132,14 @@ def test_matrix_checks():
     with pytest.raises(ValueError, match="contiguous"):
         rows(torch.zeros(40, 4).t())
     with pytest.raises(ValueError, match="contiguous"):
-        training._flat(torch.zeros(4, 80)[:, :40], torch.float32, (4, 40), x.device, "t")
+        training._flat(torch.zeros(4, 80)[:, :40], torch.float32, (4, 40), -1, "t")
     with pytest.raises(TypeError):
-        training._flat(x, torch.uint8, (4, 40), x.device, "t")
+        training._flat(x, torch.uint8, (4, 40), -1, "t")
+    with pytest.raises(ValueError, match="must be on cuda:0"):
+        training._flat(x, torch.float32, (4, 40), 0, "t")
     with pytest.raises(ValueError, match="workspace"):
-        training._workspace(x, x.device)
-    assert training._workspace(None, x.device) == (None, 0)
+        training._workspace(x, -1)
+    assert training._workspace(None, -1) == (None, 0)
 
 
 def test_a_missing_library_raises(monkeypatch, tmp_path):
