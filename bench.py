@@ -43,8 +43,8 @@ CSRC = os.path.join(ROOT, "mixed_precision_sharded_amd", "csrc")
 KERNEL_SOURCES = {
     "adamw_step_kernel": ("kernels.hip", "device.h", "layout.h"),
     "adamw_clipped_kernel": ("kernels.hip", "device.h", "layout.h"),
-    "adamw8_step_kernel": ("kernels_q8.hip", "device.h", "layout.h"),
-    "adamw8_clipped_kernel": ("kernels_q8.hip", "device.h", "layout.h"),
+    "adamw8_step_kernel": ("kernels_q8.hip", "fp8.h", "device.h", "layout.h"),
+    "adamw8_clipped_kernel": ("kernels_q8.hip", "fp8.h", "device.h", "layout.h"),
 }
 
 
