@@ -1,8 +1,13 @@
 // gfx950 kernels of the clipped policy loss, its gradient with respect to the
 // logits, and the log-probabilities of the labels.
 //
-// Every row is reduced to its largest logit and the sum of e^(x - max); one value per row (ratio, clip, KL term, the slope d loss / d l)
-// is computed in fp64, and the gradient is slope * (onehot - softmax).
+// Every row is reduced to its largest logit and the sum of e^(x - max), one
+// pass with a running maximum; one value per row (ratio, clip, KL term, the
+// slope d loss / d l) is computed in fp64, and the gradient is slope * (onehot
+// - softmax).  The logits are read and the gradient written once, 4 bytes a
+// logit in bf16, so many rows are bound by memory: 8192 x 128256 bf16 790 us
+// (5.3 TB/s), 1000 x 32003 fp32 57.7 us (4.4 TB/s).  Few rows are bound by two
+// launches that wait for one another: 24 x 128256 bf16 12.9 us.
 #include <hip/hip_runtime.h>
 
 #include "rows.h"
@@ -12,8 +17,8 @@ namespace mps {
 namespace {
 
 // Cache policy of the gradient's stores (2: nontemporal).  The rows in work
-// stay in the cache and the gradient passes it by: 8192 x 128256 bf16 811 ->
-// 795 us, 1000 x 50257 58 -> 41 us.  The logits' loads keep the default
+// stay in the cache and the gradient passes it by: with the default 8192 x
+// 128256 bf16 took 2 % longer, 1000 x 50257 58 us and not 41.  The logits' loads keep the default
 // (nontemporal, 5-40 % slower: the second reading then misses).
 constexpr int kGradientPolicy = 2;
 constexpr int kLogitsPolicy = 0;
@@ -548,22 +553,25 @@ __global__ __launch_bounds__(kBlock) void policy_total_kernel(const double* valu
 
 // Which kernel takes a call, by rows and vocabulary (measured with all of
 // them forced on the same calls, us):
-//   - up to kWaveVocab logits a row is a wavefront's: 8000 x 5000 bf16 45
-//     against 67 with a block each, 30000 x 1000 45 against 109;
+//   - up to kWaveVocab logits a row is a wavefront's: 8000 x 5000 bf16 42.6
+//     against 49.4 with a block each, 30000 x 1000 39.8 against 102.6;
 //   - above, a block's of 256 threads that reads it twice, up to kBlockVocab
-//     logits: 2000 x 9000 bf16 22.5 against 28 kept, 1000 x 12000 fp32 24
-//     against 25;
-//   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 30 against
-//     34, 8192 x 128256 bf16 811 against 1200, 2000 x 65000 fp32 231 against
-//     315; 1000 x 32003 fp32 58 against 75;
+//     logits: 2000 x 9000 bf16 20.3 (28 when it was kept), 1000 x 12000 fp32
+//     25.5 (25);
+//   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 27.4
+//     against 34.6 read twice, 8192 x 128256 bf16 790 against 1077, 2000 x
+//     65000 fp32 241 against 282, 1000 x 32003 fp32 57.7 against 65.2;
 //   - up to kFewRows rows of more than kShareVocab logits, blocks share a row:
-//     24 x 128256 bf16 14.9 against 18.8, 64 x 200000 18.6 against 28.8; but
-//     24 x 50257 14.9 against 13.7, 128 x 128256 22.6 against 20.1.
+//     24 x 128256 bf16 12.9 against 19.1 kept, 64 x 200000 15.9 against 29.1,
+//     24 x 50257 12.5 against 13.7; but 128 x 128256 22.6 against 20.1.
 constexpr int64_t kWaveVocab = 8192;
 constexpr int64_t kBlockVocab = 16384;
 constexpr int64_t kFewRows = 64;
-constexpr int64_t kShareVocab = 65536;
-constexpr int kShareLogits = 8192;  // in a share, at least
+constexpr int64_t kShareVocab = 32768;
+// Logits of a share, at most (unless lanes or blocks run out): the kDeep units
+// that each thread of a block has under way at once.  24 x 128256 bf16 13.4 us
+// with shares just above it, 14.3 with 4096.
+constexpr int kShareLogits = kDeep * kUnit * kBlock;
 constexpr int kMostBlocks = 2048;
 static_assert(kFewRows <= kWave, "a row per lane");
 
@@ -572,7 +580,7 @@ static_assert(kFewRows <= kWave, "a row per lane");
 int shares_of(int64_t rows, int64_t vocab)
 {
     if (rows <= 0 || rows > kFewRows || vocab <= kShareVocab) return 1;
-    int64_t s = vocab / kShareLogits;
+    int64_t s = (vocab + kShareLogits - 1) / kShareLogits;
     if (s > 512 / rows) s = 512 / rows;
     return static_cast<int>(s > kWave ? kWave : s);
 }

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 INF = float("inf")
 TYPES = [torch.bfloat16, torch.float32]
-SHAPES = [(1, 1), (1, 2), (3, 7), (5, 8), (2, 33), (40, 1000), (7, 2048), (300, 2051), (2, 8192), (5, 8200), (3, 32003),
+SHAPES = [(1, 1), (1, 2), (3, 7), (5, 8), (2, 33), (40, 1000), (7, 2048), (300, 2051), (2, 8192), (5, 8200), (3, 32003), (2, 32768), (3, 32769), (64, 33001), (24, 50257),
           (1, 65536), (4, 65544), (2, 128256), (3, 131072), (2, 131080), (1, 200003), (1100, 515), (2300, 64),
           # more than 64 rows: a row per block, read twice or kept, at both sides of every border and past all that is kept
           (66, 8193), (70, 9001), (65, 16384), (70, 16392), (68, 20007), (65, 32760), (66, 32768), (70, 33001), (300, 40009),
