@@ -10,6 +10,10 @@
 // of the matrix instruction wants eight t of one column.  Tiles are staged in
 // LDS as they lie (rows of t) and read with the transposing LDS load, which
 // hands each lane four t of one column.
+//
+// Large products are bound by the matrix instructions (bf16 8192 x 4096 x 4096
+// 210 us, 1310 TF/s, their pipes busy 75 % of the cycles; a chip under this
+// load lowers its clock), small ones by the stages' waits and the launch.
 #include <hip/hip_runtime.h>
 
 #include "rows.h"
