@@ -11,10 +11,13 @@
 // LDS as they lie (rows of t) and read with the transposing LDS load, which
 // hands each lane four t of one column.
 //
-// Large products are bound by the matrix instructions (bf16 8192 x 4096 x 4096
-// 210 us, 1310 TF/s, their pipes busy 75 % of the cycles; a chip under this
-// load lowers its clock), small ones by the stages' waits and the launch.
+// Large products are bound by the matrix instructions (8192 x 4096 x 4096 bf16
+// 208 us, 1320 TF/s, their pipes busy 75 % of the cycles; fp32 594 us, three
+// products at 1390 TF/s; a chip under this load lowers its clock), small ones
+// by the stages' waits and the launch (fp32 777 x 1000 x 2051 25.6 us).
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "rows.h"
 #include "train_kernels.h"
@@ -268,7 +271,9 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
 // the next stage from registers to LDS and asks memory for a share of the one
 // after that, all between its own 16 matrix instructions.  The block meets
 // once per stage, before the last step: by then every operand of the stage is
-// in registers and the next stage is in LDS.
+// in registers and the next stage is in LDS.  fp32 gradients have stages of 32
+// t, whose three parts of dy and x take the same room: six steps, 96 matrix
+// instructions for the same bytes, with the splitting beside them.
 //
 // Rows behind the last token come as zeros of both operands (the buffer
 // resources end with the split's tokens); columns behind the matrix's own
@@ -276,90 +281,108 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
 // 16-byte chunks (kAligned false: an odd width, stride or start) the last
 // chunk of a row reaches into the next row, which is harmless except in the
 // very last one: that token is left out of the stages and added to the sums
-// at the end, and the rows behind it are cleared in registers.
+// at the end, and the rows behind it are cleared in registers (8192 x 4095 x
+// 4096 bf16 240 us, fp32 630).
 
 constexpr int kWideTile = 256;
-constexpr int kWideT = 64;
-constexpr int kWideRow = kWideTile * 2;             // bytes of a staged row
-constexpr int kWideStage = kWideT * kWideRow;       // bytes of a staged operand
+constexpr int kWideRow = kWideTile * 2;  // bytes of a staged row
+constexpr int kWideBf16 = 64, kWideF32 = 32;  // t per stage
 
 __device__ __forceinline__ uint32_t wide_chunk_at(int t, int chunk)
 {
     return static_cast<uint32_t>(t * kWideRow + ((chunk ^ ((t & 3) << 2)) << 4));
 }
 
-// The order of a step's instructions: two LDS reads behind each of its first
-// eight matrix instructions and a write behind each of the next, with a load
+// The order of a step's instructions: its LDS reads behind the first eight
+// matrix instructions (two behind each if there are sixteen) and a write behind each of the next, with a load
 // from memory behind each of the first (asked for one by one, the compiler
 // gathers them before or behind the matrix instructions, which then wait:
 // 267 instead of 220 us for 8192 x 4096 x 4096; one read behind each of the
 // sixteen, with the writes last, took 238).
-template <int kWrites, int kLoads>
+template <int kReads, int kWrites, int kLoads>
 __device__ __forceinline__ void order_step()
 {
     constexpr int kMfma = 0x008, kVmemRead = 0x020, kLdsRead = 0x100, kLdsWrite = 0x200;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-        if (i < 8) __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
+        if (i < 8) __builtin_amdgcn_sched_group_barrier(kLdsRead, kReads / 8, 0);
         else if (i - 8 < kWrites) __builtin_amdgcn_sched_group_barrier(kLdsWrite, 1, 0);
         if (i < kLoads) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// A thread's share of a stage on its way from memory.
+template <bool kDyBf16>
 struct WideStage {
-    u32x4 dy[8];     // 64 x 256 bf16, eight chunks of eight per thread
-    u32x4 codes[4];  // 64 x 256 codes, four units of sixteen
-    uint32_t scale[4];
+    static constexpr int kT = kDyBf16 ? kWideBf16 : kWideF32;
+    static constexpr int kRows = kT / 8;            // units of eight of dy, eight rows apart
+    static constexpr int kUnits = kT / 16;          // units of sixteen codes, sixteen rows apart
+    u32x4 dy[8];                                    // kRows units, of one or two chunks
+    u32x4 codes[kUnits];
+    uint32_t scale[kUnits];
 };
 
-template <bool kAligned, bool kDwBf16>
+template <bool kDyBf16, bool kAligned, bool kDwBf16>
 __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, Codes x, int64_t tokens, int64_t n_all,
                                                                      int64_t k_all, int64_t per_split, uint32_t tiles_k,
                                                                      Target to)
 {
-    __shared__ __attribute__((aligned(16))) char lds[4 * kWideStage];  // dy: two stages, x: two stages
+    using Stage = WideStage<kDyBf16>;
+    constexpr int kT = Stage::kT, kE = kDyBf16 ? 2 : 4, kParts = kDyBf16 ? 1 : 3;
+    constexpr int kOperand = kT * kWideRow;            // bytes of a staged operand
+    constexpr int kX = 2 * kParts * kOperand;          // dy's parts: two stages, then x: two stages
+    __shared__ __attribute__((aligned(16))) char lds[kX + 2 * kOperand];
     const Tile tile = tile_of(blockIdx.x, gridDim.x, tiles_k);
     const int64_t n0 = tile.n * kWideTile;
     const int64_t k0 = tile.k * kWideTile;
     const int64_t padded = (k_all + kRun - 1) / kRun * kRun;
     const int64_t t_first = blockIdx.y * per_split;
     const int64_t t_last = min(t_first + per_split, kAligned ? tokens : tokens - 1);
-    const int stages = static_cast<int>((t_last - t_first + kWideT - 1) / kWideT);
+    const int stages = static_cast<int>((t_last - t_first + kT - 1) / kT);
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int wn = wave / 2 * 128, wk = wave % 2 * 128;
 
     // Where this thread's share of a stage lies, in bytes from the stage's first row.
-    const uint32_t dy_row = static_cast<uint32_t>(dy.stride) * 2u, x_row = static_cast<uint32_t>(padded);
-    const uint32_t dy_off = (tid / 32) * dy_row + (tid % 32) * 16u;     // + 8 rows per chunk
+    const uint32_t dy_row = static_cast<uint32_t>(dy.stride) * kE, x_row = static_cast<uint32_t>(padded);
+    const uint32_t dy_off = (tid / 32) * dy_row + (tid % 32) * 8u * kE;  // + 8 rows per unit
     const uint32_t x_off = (tid / 16) * x_row + (tid % 16) * 16u;       // + 16 rows per unit
     const uint32_t s_off = (tid / 16) * (x_row / 32) + (tid % 16) / 2;
-    const char* dy_base = static_cast<const char*>(dy.data) + n0 * 2;
+    const char* dy_base = static_cast<const char*>(dy.data) + n0 * kE;
     const uint8_t* x_base = x.codes + k0;
     const uint8_t* s_base = x.scales + k0 / kRun;
 
     // The operands' bytes behind a stage's first row, `row` for each of its tokens and `less` fewer in the last one; the
     // stage behind the split's tokens, and those that follow, reach nothing.
     const int t_count = static_cast<int>(max(t_last - t_first, static_cast<int64_t>(0)));
-    const int whole = t_count / kWideT, rest = t_count % kWideT;
-    const uint32_t dy_less = static_cast<uint32_t>((dy.stride - n_all + n0) * 2), x_less = static_cast<uint32_t>(k0);
+    const int whole = t_count / kT, rest = t_count % kT;
+    const uint32_t dy_less = static_cast<uint32_t>((dy.stride - n_all + n0) * kE), x_less = static_cast<uint32_t>(k0);
     auto reach = [&](int s, uint32_t row, uint32_t less) {
         const uint32_t last = rest ? rest * row - less : 0u;
-        return s < whole ? kWideT * row - less : (s == whole ? last : 0u);
+        return s < whole ? kT * row - less : (s == whole ? last : 0u);
     };
     const char* dy_stage = dy_base + t_first * dy_row;
     const uint8_t* x_stage = x_base + t_first * x_row;
     const uint8_t* s_stage = s_base + t_first * (x_row / 32);
-    auto load_dy = [&](WideStage& w, int s, const char* at, int first, int count) {
-        // Not aligned: to the end of the matrix, which the last stages reach.
-        const int64_t left = kAligned ? 0 : (tokens - t_first - static_cast<int64_t>(s) * kWideT) * dy_row - dy_less;
-        const __amdgpu_buffer_rsrc_t r = rsrc(at, kAligned ? reach(s, dy_row, dy_less)
-                                                           : static_cast<uint32_t>(left < 0 ? 0 : min(left, 2ll * kWideT * dy_row)));
+    auto load_dy = [&](Stage& w, int s, const char* at, int first, int count) __attribute__((always_inline)) {
+        uint32_t bytes = 0;
+        if (kAligned) {
+            bytes = reach(s, dy_row, dy_less);
+        } else {  // to the end of the matrix, which the last stages reach
+            const int64_t left = (tokens - t_first - static_cast<int64_t>(s) * kT) * dy_row - dy_less;
+            const uint32_t most = left < 0 ? 0u : static_cast<uint32_t>(min(left, static_cast<int64_t>(2 * kT) * dy_row));
+            // Said to be uniform: each load would be a loop over the lanes' resources otherwise.
+            bytes = __builtin_amdgcn_readfirstlane(most);
+        }
+        const __amdgpu_buffer_rsrc_t r = rsrc(at, bytes);
 #pragma unroll
-        for (int j = first; j < first + count; ++j) w.dy[j] = load_u32x4<0>(r, dy_off + j * 8 * dy_row);
+        for (int j = first; j < first + count; ++j) {
+#pragma unroll
+            for (int h = 0; h < kE / 2; ++h) w.dy[j * (kE / 2) + h] = load_u32x4<0>(r, dy_off + j * 8 * dy_row + h * 16);
+        }
     };
-    auto load_x = [&](WideStage& w, int s, const uint8_t* at, const uint8_t* scales_at, int first, int count) {
+    auto load_x = [&](Stage& w, int s, const uint8_t* at, const uint8_t* scales_at, int first, int count) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t r = rsrc(at, reach(s, x_row, x_less));
         const __amdgpu_buffer_rsrc_t rs = rsrc(scales_at, reach(s, x_row / 32, x_less / 32));
 #pragma unroll
@@ -372,20 +395,30 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
     // A unit fills two chunks.  Eight lanes write at a time; the last four of them take their second chunk first, so
     // that the eight are spread over all banks (with every lane's first chunk first, each write took twice as long).
     const bool swap = tid & 4;
-    const uint32_t x_at = 2 * kWideStage + wide_chunk_at(tid / 16, tid % 16 * 2) + (swap ? 16 : 0);  // + 16 rows
+    const uint32_t x_at = kX + wide_chunk_at(tid / 16, tid % 16 * 2) + (swap ? 16 : 0);  // + 16 rows
     const uint32_t x_at2 = x_at ^ 16;
-    auto put_dy = [&](const WideStage& w, int s, int buf, int first, int count) {
+    auto put_dy = [&](const Stage& w, int s, int buf, int first, int count) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = first; j < first + count; ++j) {
-            u32x4 v = w.dy[j];
-            if (!kAligned) {
-                const uint32_t keep = s * kWideT + tid / 32 + j * 8 < t_count ? ~0u : 0u;
-                v = v & u32x4{keep, keep, keep, keep};
+            Raw8<kDyBf16> raw;
+#pragma unroll
+            for (int h = 0; h < kE / 2; ++h) {
+                raw.v[h] = w.dy[j * (kE / 2) + h];
+                if (!kAligned) {
+                    const uint32_t keep = s * kT + tid / 32 + j * 8 < t_count ? ~0u : 0u;
+                    raw.v[h] = raw.v[h] & u32x4{keep, keep, keep, keep};
+                }
             }
-            *reinterpret_cast<u32x4*>(lds + buf * kWideStage + dy_at + j * 8 * kWideRow) = v;
+            u32x4 part[3];
+            if constexpr (kDyBf16) part[0] = raw.v[0];
+            else split3(raw, part);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                *reinterpret_cast<u32x4*>(lds + (buf * kParts + p) * kOperand + dy_at + j * 8 * kWideRow) = part[p];
+            }
         }
     };
-    auto put_x = [&](const WideStage& w, int buf, int first, int count) {
+    auto put_x = [&](const Stage& w, int buf, int first, int count) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = first; j < first + count; ++j) {
             const float scale = __uint_as_float(w.scale[j] << 23);
@@ -398,7 +431,7 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
                     v[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, false));
                     v[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, true));
                 }
-                *reinterpret_cast<u32x4*>(lds + buf * kWideStage + (h == 0 ? x_at : x_at2) + j * 16 * kWideRow) = v;
+                *reinterpret_cast<u32x4*>(lds + buf * kOperand + (h == 0 ? x_at : x_at2) + j * 16 * kWideRow) = v;
             }
         }
     };
@@ -411,13 +444,13 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
         for (int i = 0; i < 4; ++i) {
             const uint32_t at = t * kWideRow + (((i ^ (t & 3)) * 4 + low) << 4) + l16 % 2 * 8;
             a_at[i] = at + wn * 2;
-            b_at[i] = at + wk * 2 + 2 * kWideStage;
+            b_at[i] = at + wk * 2 + kX;
         }
     }
-    auto read4 = [&](bf16x8 (&v)[4], const uint32_t (&at)[4], int buf, int step) {
+    auto read4 = [&](bf16x8 (&v)[4], const uint32_t (&at)[4], int offset) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const char* p = lds + at[i] + buf * kWideStage + step * 16 * kWideRow;
+            const char* p = lds + at[i] + offset;
             const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                                              (__attribute__((address_space(3))) s16x4*)p));
             const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -428,57 +461,104 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
 
     f32x16 acc[4][4] = {};
     bf16x8 a[2][4], b[2][4];
-    WideStage w;
-    auto multiply = [&](int h) {
+    Stage w;
+    auto read_a = [&](int h, int buf, int step, int part) __attribute__((always_inline)) {
+        read4(a[h], a_at, (buf * kParts + part) * kOperand + step * 16 * kWideRow);
+    };
+    auto read_b = [&](int h, int buf, int step) __attribute__((always_inline)) { read4(b[h], b_at, buf * kOperand + step * 16 * kWideRow); };
+    auto multiply = [&](int ha, int hb) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[ha][i], b[hb][j], acc[i][j], 0, 0, 0);
         }
     };
-    const int64_t dy_step = static_cast<int64_t>(kWideT) * dy_row, x_step = static_cast<int64_t>(kWideT) * x_row;
-    load_dy(w, 0, dy_stage, 0, 8);
-    load_x(w, 0, x_stage, s_stage, 0, 4);
-    put_dy(w, 0, 0, 0, 8);
-    put_x(w, 0, 0, 4);
-    // From here on the pointers are at the stage behind the one in work: its last two units of x are still to come.
-    dy_stage += dy_step, x_stage += x_step, s_stage += x_step / 32;
-    load_dy(w, 1, dy_stage, 0, 8);
+    const int64_t dy_step = static_cast<int64_t>(kT) * dy_row, x_step = static_cast<int64_t>(kT) * x_row;
+    auto advance = [&]() __attribute__((always_inline)) { dy_stage += dy_step, x_stage += x_step, s_stage += x_step / 32; };
+    load_dy(w, 0, dy_stage, 0, Stage::kRows);
+    load_x(w, 0, x_stage, s_stage, 0, Stage::kUnits);
+    put_dy(w, 0, 0, 0, Stage::kRows);
+    put_x(w, 0, 0, Stage::kUnits);
+    // From here on the pointers are, for bf16, at the stage behind the one in work, whose last two units of x are still to
+    // come, and for fp32 at the one after that.
+    advance();
+    load_dy(w, 1, dy_stage, 0, Stage::kRows);
     load_x(w, 1, x_stage, s_stage, 0, 2);
+    if (!kDyBf16) advance();
     __syncthreads();
-    read4(a[0], a_at, 0, 0);
-    read4(b[0], b_at, 0, 0);
+    read_a(0, 0, 0, 0);
+    read_b(0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    auto stage = [&](int s, int buf) {
-        read4(a[1], a_at, buf, 1);
-        read4(b[1], b_at, buf, 1);
+    auto stage_bf16 = [&](int s, int buf) __attribute__((always_inline)) {
+        read_a(1, buf, 1, 0);
+        read_b(1, buf, 1);
         load_x(w, s + 1, x_stage, s_stage, 2, 2);
-        multiply(0);
+        multiply(0, 0);
         put_dy(w, s + 1, buf ^ 1, 0, 4);
         put_x(w, buf ^ 1, 0, 1);
-        dy_stage += dy_step, x_stage += x_step, s_stage += x_step / 32;
-        order_step<6, 4>();
-        read4(a[0], a_at, buf, 2);
-        read4(b[0], b_at, buf, 2);
+        advance();
+        order_step<16, 6, 4>();
+        read_a(0, buf, 2, 0);
+        read_b(0, buf, 2);
         load_dy(w, s + 2, dy_stage, 0, 4);
         load_x(w, s + 2, x_stage, s_stage, 0, 1);
-        multiply(1);
+        multiply(1, 1);
         put_dy(w, s + 1, buf ^ 1, 4, 4);
         put_x(w, buf ^ 1, 1, 1);
-        order_step<6, 6>();
-        read4(a[1], a_at, buf, 3);
-        read4(b[1], b_at, buf, 3);
+        order_step<16, 6, 6>();
+        read_a(1, buf, 3, 0);
+        read_b(1, buf, 3);
         load_dy(w, s + 2, dy_stage, 4, 4);
         load_x(w, s + 2, x_stage, s_stage, 1, 1);
-        multiply(0);
+        multiply(0, 0);
         put_x(w, buf ^ 1, 2, 2);
-        order_step<4, 6>();
+        order_step<16, 4, 6>();
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        read4(a[0], a_at, buf ^ 1, 0);
-        read4(b[0], b_at, buf ^ 1, 0);
-        multiply(1);
-        order_step<0, 0>();
+        read_a(0, buf ^ 1, 0, 0);
+        read_b(0, buf ^ 1, 0);
+        multiply(1, 1);
+        order_step<16, 0, 0>();
+    };
+    // fp32: six steps, each part of dy for each of the two sixteens of t; what a step puts away, the next one asks for.
+    auto stage_f32 = [&](int s, int buf) __attribute__((always_inline)) {
+        read_a(1, buf, 0, 1);
+        multiply(0, 0);
+        put_dy(w, s + 1, buf ^ 1, 0, 1);
+        order_step<8, 3, 0>();
+        read_a(0, buf, 0, 2);
+        load_dy(w, s + 2, dy_stage, 0, 1);
+        multiply(1, 0);
+        put_dy(w, s + 1, buf ^ 1, 1, 1);
+        order_step<8, 3, 2>();
+        read_a(1, buf, 1, 0);
+        read_b(1, buf, 1);
+        load_dy(w, s + 2, dy_stage, 1, 1);
+        multiply(0, 0);
+        put_x(w, buf ^ 1, 0, 2);
+        order_step<16, 4, 2>();
+        read_a(0, buf, 1, 1);
+        load_x(w, s + 2, x_stage, s_stage, 0, 2);
+        multiply(1, 1);
+        put_dy(w, s + 1, buf ^ 1, 2, 1);
+        order_step<8, 3, 4>();
+        read_a(1, buf, 1, 2);
+        load_dy(w, s + 2, dy_stage, 2, 1);
+        multiply(0, 1);
+        put_dy(w, s + 1, buf ^ 1, 3, 1);
+        order_step<8, 3, 2>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        read_a(0, buf ^ 1, 0, 0);
+        read_b(0, buf ^ 1, 0);
+        load_dy(w, s + 2, dy_stage, 3, 1);
+        multiply(1, 1);
+        advance();
+        order_step<16, 0, 2>();
+    };
+    auto stage = [&](int s, int buf) __attribute__((always_inline)) {
+        if constexpr (kDyBf16) stage_bf16(s, buf);
+        else stage_f32(s, buf);
     };
     // Two stages a round, so that the buffers' addresses are constants of the code (4 % faster).
     int s = 0;
@@ -495,12 +575,15 @@ __global__ __launch_bounds__(kBlock, 1) void weight_grad_wide_kernel(Matrix dy, 
             const int64_t k = min(k0 + wk + j * kFrag + lane % 32, padded - 1);
             xv[j] = decode1<true>(x.codes[t * padded + k], scale_value(x.scales[t * (padded / kRun) + k / kRun]));
         }
-        const uint16_t* last = static_cast<const uint16_t*>(dy.data) + t * dy.stride;
+        auto last = [&](int64_t n) {
+            if (kDyBf16) return bf16_lo(static_cast<const uint16_t*>(dy.data)[t * dy.stride + n]);
+            return static_cast<const float*>(dy.data)[t * dy.stride + n];
+        };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const float d = bf16_lo(last[min(n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4, n_all - 1)]);
+                const float d = last(min(n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4, n_all - 1));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j][r] = __builtin_fmaf(d, xv[j], acc[i][j][r]);
             }
@@ -540,7 +623,7 @@ struct TileKind {
     int edge, stage_t;
     double alone_us, shared_us;
 };
-constexpr TileKind kWide = {kWideTile, kWideT, 1.6, 1.6};  // one block fills a CU
+constexpr TileKind kWide[2] = {{kWideTile, kWideF32, 2.3, 2.3}, {kWideTile, kWideBf16, 1.6, 1.6}};  // one block fills a CU
 constexpr TileKind kMid[2] = {{128, kStageF32, 1.14, 0.84}, {128, kStageBf16, 1.0, 0.70}};  // [bf16]
 constexpr TileKind kSmall[2] = {{64, kStageF32, 0.60, 0.30}, {64, kStageBf16, 0.54, 0.29}};
 
@@ -555,13 +638,14 @@ struct Plan {
 // to memory and back (4 TB/s) and their join.  With each choice forced (us):
 // 8192 x 4096 x 4096 bf16 207 wide, 358 at 128, 585 at 64; 2048 x 4096 x 1024
 // 40, 36, 40; 1000 x 1000 x 1000 19.7, 16.3 and 10.8; fp32 777 x 1000 x 2051 31
-// and 26.5, 8192 x 4096 x 4096 860 and 1222.
+// at 128 and 25.6 at 64, 2048 x 4096 x 4096 157 wide and 223 at 128, 8192 x
+// 4096 x 4096 594, 868 and 1222.
 Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
 {
     Plan best;
     double least = 0.0;
     const double values = static_cast<double>(n) * static_cast<double>(k);
-    for (const TileKind& kind : {kSmall[bf16], kMid[bf16], kWide}) {
+    for (const TileKind& kind : {kSmall[bf16], kMid[bf16], kWide[bf16]}) {
         if (kind.edge == kWideTile && !wide) continue;
         const int64_t tiles_n = (n + kind.edge - 1) / kind.edge, tiles_k = (k + kind.edge - 1) / kind.edge;
         const int64_t stages = (tokens + kind.stage_t - 1) / kind.stage_t;
@@ -584,16 +668,16 @@ Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
 }
 
 // Whether dy's rows are whole 16-byte chunks.
-bool chunk_rows(const Matrix& dy, int64_t n)
+bool chunk_rows(const Matrix& dy, bool bf16, int64_t n)
 {
-    return n % 8 == 0 && dy.stride % 8 == 0 && reinterpret_cast<uintptr_t>(dy.data) % 16 == 0;
+    const int64_t chunk = bf16 ? 8 : 4;
+    return n % chunk == 0 && dy.stride % chunk == 0 && reinterpret_cast<uintptr_t>(dy.data) % 16 == 0;
 }
 
-// The wide tile takes bf16 gradients of rows that keep two stages' offsets
-// below 2^32 bytes.
+// The wide tile takes rows that keep two stages' offsets below 2^32 bytes.
 bool wide_fits(int64_t dy_stride, bool dy_bf16, int64_t n, int64_t k)
 {
-    return dy_bf16 && dy_stride < 1 << 23 && n >= 64 && k >= 64 && k <= 1 << 25;
+    return dy_stride < 1 << (dy_bf16 ? 23 : 22) && n >= 64 && k >= 64 && k <= 1 << 25;
 }
 
 size_t scratch_of(const Plan& s, int64_t n, int64_t k)
@@ -607,10 +691,12 @@ size_t scratch_of(const Plan& s, int64_t n, int64_t k)
 size_t weight_grad_scratch(int64_t tokens, int64_t out_features, int64_t in_features)
 {
     size_t most = 0;
-    for (int i = 0; i < 3; ++i) {  // fp32; bf16 without and with the wide tile
-        const bool wide = i == 2 && wide_fits(out_features, true, out_features, in_features);
-        const size_t need = scratch_of(plan_of(tokens, out_features, in_features, i > 0, wide), out_features, in_features);
-        if (need > most) most = need;
+    for (const bool bf16 : {false, true}) {
+        for (const bool wide : {false, true}) {
+            if (wide && !wide_fits(out_features, bf16, out_features, in_features)) continue;
+            const size_t need = scratch_of(plan_of(tokens, out_features, in_features, bf16, wide), out_features, in_features);
+            if (need > most) most = need;
+        }
     }
     return most;
 }
@@ -628,13 +714,14 @@ hipError_t launch_act8_weight_grad(Matrix dy, bool dy_bf16, Codes x, int64_t tok
                                             Target{dw, partials, accumulate, out_features, in_features});
     };
     if (s.edge == kWideTile) {
-        if (chunk_rows(dy, out_features)) {
-            if (dw_bf16) run(weight_grad_wide_kernel<true, true>);
-            else run(weight_grad_wide_kernel<true, false>);
-        } else {
-            if (dw_bf16) run(weight_grad_wide_kernel<false, true>);
-            else run(weight_grad_wide_kernel<false, false>);
-        }
+        auto wide = [&](auto bf16, auto aligned) {
+            if (dw_bf16) run(weight_grad_wide_kernel<bf16.value, aligned.value, true>);
+            else run(weight_grad_wide_kernel<bf16.value, aligned.value, false>);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (chunk_rows(dy, dy_bf16, out_features)) dy_bf16 ? wide(yes, yes) : wide(no, yes);
+        else dy_bf16 ? wide(yes, no) : wide(no, no);
     } else if (s.edge == 128) {
         if (dy_bf16) {
             if (dw_bf16) run(weight_grad_kernel<true, true, 128>);

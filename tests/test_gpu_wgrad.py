@@ -22,7 +22,10 @@ SHAPES = [(1, 1, 1), (5, 3, 7), (31, 33, 32), (32, 128, 128), (33, 129, 131), (6
           # tiles of 128, without and with splits of the tokens
           (2048, 2048, 2048), (3000, 1025, 2050),
           # bf16 gradients: tiles of 256, with splits and without, rows of whole 16-byte chunks and odd ones
-          (4000, 1032, 2056), (4000, 1031, 2056), (600, 4096, 4352), (700, 4099, 4100)]
+          (4000, 1032, 2056), (4000, 1031, 2056), (600, 4096, 4352), (700, 4099, 4100),
+          # the same for fp32 gradients
+          (1, 4096, 4096), (33, 4096, 4100), (450, 2300, 4099), (1000, 2051, 4099), (2047, 2050, 2056), (6000, 1028, 1030),
+          (6000, 1031, 1030)]
 
 
 def gen(seed):
@@ -111,7 +114,8 @@ def test_fp32_gradients_keep_all_their_bits(oracle_lib):
 
 
 @pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 70, 150, 160), (torch.float32, 70, 150, 160),
-                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 700, 4099, 4100)])
+                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 700, 4099, 4100),
+                                         (torch.float32, 450, 2300, 4099), (torch.float32, 1000, 2051, 4099)])
 def test_nonfinite_values_stay_in_their_rows_and_columns(oracle_lib, dtype, t, n, k):
     x = torch.ones(t, k)
     x[3, 40] = float("nan")  # the run of columns 32 .. 63
@@ -154,7 +158,8 @@ def test_two_runs_give_the_same_bits(oracle_lib, t, n, k):
 
 
 @pytest.mark.parametrize("dtype,t,n,k", [(torch.bfloat16, 40, 64, 64), (torch.float32, 40, 64, 64),
-                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 257, 1024, 1024)])
+                                         (torch.bfloat16, 600, 4096, 4352), (torch.bfloat16, 257, 1024, 1024),
+                                         (torch.float32, 1030, 4096, 4096)])
 def test_offsets_past_32_bits(oracle_lib, dtype, t, n, k):
     """dy with more than 2^32 elements: a stride that puts the last tokens far out
     (in steps of less and of more than 2^25 elements)."""
