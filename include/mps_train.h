@@ -144,7 +144,7 @@ int act8_swiglu_backward(const void* d_dout, mps_dtype dtype, int64_t dout_strid
  * formed exactly and summed in fp32 by the matrix cores (bf16 operands; the
  * one rounding on the way in is that of kept values below 2^-126, which bf16
  * holds with fewer bits).  fp32 gradients enter as three bf16 parts each,
- * which hold all their 24 bits.  dw is rounded once, after the sum with what
+ * which hold all their 24 bits down to 2^-133.  dw is rounded once, after the sum with what
  * it held.
  *   dy_dtype   : MPS_DTYPE_F32 or MPS_DTYPE_BF16.
  *   d_dw       : fp32 or bf16 (dw_dtype) [out_features, in_features], e.g.
