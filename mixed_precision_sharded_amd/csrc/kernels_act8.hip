@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kBlock) void act8_load_kernel(Codes in, int64_t row
         float v[kUnit];
         const int64_t c = static_cast<int64_t>(w.col) * kUnit;
         load_codes(in.codes, in.scales, w.unit(), v);
-        store8<kBf16>(v, x.data, w.row * x.stride + c, cols - c);
+        store_unit<kBf16>(v, x.data, w.row * x.stride + c, cols - c);
     }
 }
 
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kBlock) void act8_swiglu_kernel(Matrix gate, Matrix
         store_codes<true>(u, kept_up.codes, kept_up.scales, w.unit());
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
-        store8<kBf16>(o, out.data, w.row * out.stride + c, cols - c);
+        store_unit<kBf16>(o, out.data, w.row * out.stride + c, cols - c);
     }
 }
 
@@ -114,8 +114,8 @@ __global__ __launch_bounds__(kBlock) void act8_swiglu_backward_kernel(
             dg[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
             du[i] = d[i] * gs;
         }
-        store8<kBf16>(dg, dgate.data, w.row * dgate.stride + c, cols - c);
-        store8<kBf16>(du, dup.data, w.row * dup.stride + c, cols - c);
+        store_unit<kBf16>(dg, dgate.data, w.row * dgate.stride + c, cols - c);
+        store_unit<kBf16>(du, dup.data, w.row * dup.stride + c, cols - c);
         if (out.codes) {
             // Behind the row's end the kept bytes may hold anything.
 #pragma unroll
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(Team<kThreads>::kBlockThreads) void act8_rmsnorm_ke
             float o[kUnit];
 #pragma unroll
             for (int i = 0; i < kUnit; ++i) o[i] = v[j][i] * r * w[j][i];
-            store8<kBf16>(o, y.data, row * y.stride + c, cols - c);
+            store_unit<kBf16>(o, y.data, row * y.stride + c, cols - c);
         }
     }
 }
@@ -234,7 +234,7 @@ __device__ __forceinline__ void norm_dx(const float (&d)[kUnit], const float (&x
         o[i] = r * (d[i] * w[i] - xh[i] * mean);
         if (residual) o[i] += res[i];
     }
-    store8<kBf16>(o, dx.data, row * dx.stride + c, cols - c);
+    store_unit<kBf16>(o, dx.data, row * dx.stride + c, cols - c);
 }
 
 // Block b leaves its rows' share of dweight in row b of `partials`.

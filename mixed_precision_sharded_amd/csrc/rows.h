@@ -133,6 +133,34 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x)
     return x;
 }
 
+// store8 of a unit of a row, by the quads of lanes that hold its runs (they
+// come here together).  An fp32 unit is two stores of 16 bytes; of a whole run
+// the lanes first exchange, so that each of its two stores is 64 bytes in one
+// piece and not every other 16 of 128 (fp32 8192 x 8192 kept and read back 158
+// -> 133 us, RMSNorm 119 -> 105, SwiGLU backward 4096 x 8192 96.8 -> 91.2; not
+// so RMSNorm of rows of 20000, 41.9 -> 43.4, which takes store8).
+template <bool kBf16>
+__device__ __forceinline__ void store_unit(const float (&x)[kUnit], void* base, int64_t at, int64_t n)
+{
+    const int q = threadIdx.x % 4;
+    if (kBf16 || n + q * kUnit < kRun) return store8<kBf16>(x, base, at, n);
+    constexpr int kLower = 0x50, kUpper = 0xfa;  // quad_perm [0,0,1,1] and [2,2,3,3]
+    u32x4_at4 first, second;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int lo = __float_as_int(x[i]), hi = __float_as_int(x[4 + i]);
+        const int a = __builtin_amdgcn_update_dpp(0, lo, kLower, 0xf, 0xf, false);
+        const int b = __builtin_amdgcn_update_dpp(0, hi, kLower, 0xf, 0xf, false);
+        const int c = __builtin_amdgcn_update_dpp(0, lo, kUpper, 0xf, 0xf, false);
+        const int d = __builtin_amdgcn_update_dpp(0, hi, kUpper, 0xf, 0xf, false);
+        first[i] = static_cast<uint32_t>(q & 1 ? b : a);
+        second[i] = static_cast<uint32_t>(q & 1 ? d : c);
+    }
+    auto* p = reinterpret_cast<u32x4_at4*>(static_cast<float*>(base) + at - q * (kUnit / 2));
+    __builtin_nontemporal_store(first, p);
+    __builtin_nontemporal_store(second, p + 4);
+}
+
 // Encode this lane's eight elements, the quad's lanes holding one run, and
 // store them as unit `unit` of the matrix (eight codes; the quad's first
 // lane writes the scale byte).  The four lanes come here together.
