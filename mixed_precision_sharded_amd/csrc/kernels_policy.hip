@@ -6,7 +6,7 @@
 // slope d loss / d l) is computed in fp64, and the gradient is slope * (onehot
 // - softmax).  The logits are read and the gradient written once, 4 bytes a
 // logit in bf16, so many rows are bound by memory: 8192 x 128256 bf16 790 us
-// (5.3 TB/s), 1000 x 32003 fp32 57.7 us (4.4 TB/s).  Few rows are bound by two
+// (5.3 TB/s), 4000 x 32003 fp32 205 us (5.0 TB/s).  Few rows are bound by two
 // launches that wait for one another: 24 x 128256 bf16 12.9 us.
 #include <hip/hip_runtime.h>
 
@@ -585,10 +585,10 @@ __global__ __launch_bounds__(kBlock) void policy_total_kernel(const double* valu
 //     against 49.4 with a block each, 30000 x 1000 39.8 against 102.6;
 //   - above, a block's of 256 threads that reads it twice, up to kBlockVocab
 //     logits: 2000 x 9000 bf16 20.3 (28 when it was kept), 1000 x 12000 fp32
-//     25.5 (25);
+//     23.9 (25);
 //   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 27.4
 //     against 34.6 read twice, 8192 x 128256 bf16 790 against 1077, 2000 x
-//     65000 fp32 241 against 282, 1000 x 32003 fp32 57.7 against 65.2;
+//     65000 fp32 218 against 275, 1000 x 32003 fp32 49.5 against 56.5;
 //   - up to kFewRows rows of more than kShareVocab logits, blocks share a row:
 //     24 x 128256 bf16 12.9 against 19.1 kept, 64 x 200000 15.9 against 29.1,
 //     24 x 50257 12.5 against 13.7; but 128 x 128256 22.6 against 20.1.
