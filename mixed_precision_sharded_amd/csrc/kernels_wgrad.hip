@@ -633,13 +633,17 @@ struct Plan {
     int splits;
 };
 
+// Partial sums, at most: a workspace of 256 MB.  fp32 16384 x 14336 x 4096
+// takes 4.81 ms for it and 4.43 split in two, with 470 MB.
+constexpr double kMostPartials = 1 << 26;
+
 // The tile and the count of splits of the tokens under which the work should
 // take least: the busiest CU's stages, and with splits the partial sums' way
 // to memory and back (4 TB/s) and their join.  With each choice forced (us):
 // 8192 x 4096 x 4096 bf16 207 wide, 358 at 128, 585 at 64; 2048 x 4096 x 1024
 // 40, 36, 40; 1000 x 1000 x 1000 19.7, 16.3 and 10.8; fp32 777 x 1000 x 2051 31
 // at 128 and 25.6 at 64, 2048 x 4096 x 4096 157 wide and 223 at 128, 8192 x
-// 4096 x 4096 594, 868 and 1222.
+// 4096 x 4096 594, 868 and 1222. 
 Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
 {
     Plan best;
@@ -649,7 +653,7 @@ Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
         if (kind.edge == kWideTile && !wide) continue;
         const int64_t tiles_n = (n + kind.edge - 1) / kind.edge, tiles_k = (k + kind.edge - 1) / kind.edge;
         const int64_t stages = (tokens + kind.stage_t - 1) / kind.stage_t;
-        for (int64_t c = 1; c <= 32 && (c == 1 || 2 * c <= stages); ++c) {
+        for (int64_t c = 1; c <= 32 && (c == 1 || (2 * c <= stages && static_cast<double>(c) * values <= kMostPartials)); ++c) {
             const int64_t each = (stages + c - 1) / c;
             const double on_cu = static_cast<double>((tiles_n * tiles_k * c + 255) / 256) * kind.shared_us;
             const double cost = static_cast<double>(each) * (on_cu > kind.alone_us ? on_cu : kind.alone_us) +
