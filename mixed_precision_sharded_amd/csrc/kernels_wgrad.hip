@@ -643,7 +643,7 @@ constexpr double kMostPartials = 1 << 26;
 // 8192 x 4096 x 4096 bf16 207 wide, 358 at 128, 585 at 64; 2048 x 4096 x 1024
 // 40, 36, 40; 1000 x 1000 x 1000 19.7, 16.3 and 10.8; fp32 777 x 1000 x 2051 31
 // at 128 and 25.6 at 64, 2048 x 4096 x 4096 157 wide and 223 at 128, 8192 x
-// 4096 x 4096 594, 868 and 1222. 
+// 4096 x 4096 594, 868 and 1222.
 Plan plan_of(int64_t tokens, int64_t n, int64_t k, bool bf16, bool wide)
 {
     Plan best;
