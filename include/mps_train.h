@@ -168,7 +168,9 @@ int act8_weight_grad(const void* d_dy, mps_dtype dy_dtype, int64_t dy_stride,
  *     *d_loss = sum over t of loss_t
  *     dlogits = (d loss_t / d l) * (onehot(label) - softmax(x))
  * where the min gives both sides at a tie, the gradient of the unclipped one.
- * An advantage of 0 contributes nothing to either, whatever the ratio.
+ * An advantage of 0 contributes nothing to either, whatever the ratio, and a
+ * kl_coef of 0 nothing, whatever the KL term: with ref_logp given, token_kl is
+ * then written and loss and gradient are those of the call without it.
  * Row statistics in fp32 with fp64 sums, one value per row in fp64; outputs
  * rounded once.
  *

@@ -106,8 +106,10 @@ __device__ __attribute__((noinline)) RowResult row_values(float top, double sum,
         const double q = exp(d);
         const double kl = q == INFINITY ? q : q - d - 1.0;  // the label has no probability left
         r.kl = static_cast<float>(kl);
-        gain -= kl_coef * kl;
-        slope += kl_coef * (1.0 - q);
+        if (kl_coef != 0.0) {  // else the term is only watched: no 0 * inf of it in the loss
+            gain -= kl_coef * kl;
+            slope += kl_coef * (1.0 - q);
+        }
     }
     r.loss = -w * gain;
     slope *= w;
