@@ -43,23 +43,25 @@ _SIZES = {
     "act8_weight_grad_workspace_bytes": (_I64, _I64, _I64),
     "policy_loss_workspace_bytes": (_I64, _I64),
 }
-_bound = None
-_functions = {}
+# (library, its entry points by name), replaced as a whole: threads that come
+# here for the first time at once each see one that is complete.
+_bound = (object(), {})
 
 
 def _function(name: str):
     """The library's entry point, with its C types."""
     global _bound
     lib = binding.lib()
-    if _bound is not lib:
-        _functions.clear()
+    bound = _bound
+    if bound[0] is not lib:
+        functions = {}
         for names, restype in ((_SIGNATURES, ctypes.c_int), (_SIZES, ctypes.c_size_t)):
             for n, argtypes in names.items():
                 f = getattr(lib, n)
                 f.argtypes, f.restype = argtypes, restype
-                _functions[n] = f
-        _bound = lib
-    return _functions[name]
+                functions[n] = f
+        _bound = bound = (lib, functions)
+    return bound[1][name]
 
 
 # A call's checks cost the host about as much as its launch, so they are kept
@@ -78,7 +80,8 @@ def _enqueue(name: str, device: int, stream: Optional[torch.cuda.Stream], *args)
         if stream.device.index != device:
             raise ValueError(f"stream: of {stream.device}, with tensors on cuda:{device}")
         handle = stream.cuda_stream
-    f = _functions[name] if _bound is binding._lib and _bound is not None else _function(name)
+    bound = _bound
+    f = bound[1][name] if bound[0] is binding._lib else _function(name)
     if _current_device() == device:
         rc = f(*args, handle)
     else:
