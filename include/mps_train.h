@@ -113,6 +113,8 @@ int act8_rmsnorm_backward(const void* d_dy, mps_dtype dy_dtype, int64_t dy_strid
 /*
  * act8_swiglu — out = gate * sigmoid(gate) * up, keeping gate and up in 8
  * bits.  gate and up may be the two halves of one matrix (the same stride).
+ * Products in fp32, out rounded once; a sigmoid below fp32's normal range,
+ * 2^-126 (a gate below -87.3), counts as 0, also in the backward pass.
  *   dtype : the type of gate, up and out.
  */
 int act8_swiglu(const void* d_gate, int64_t gate_stride, const void* d_up, int64_t up_stride,

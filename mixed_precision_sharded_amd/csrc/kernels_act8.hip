@@ -61,14 +61,15 @@ __global__ __launch_bounds__(kBlock) void act8_load_kernel(Codes in, int64_t row
 
 // 1 / (1 + e^-g).  The exponent -g log2(e) is rounded to n, and what the
 // rounding lost is put back to first order, so the error stays near the two
-// instructions' own (1 ulp each) for every g; far out, where 2^n is 0 or
-// infinite and the correction would be inf * 0, it is left out.
+// instructions' own (1 ulp each).  From |n| = 128 on, where 2^n is 0 or
+// infinite and the correction would be inf * 0, it is left out.  The reciprocal
+// gives 0 for results below fp32's normal range, 2^-126: g below -87.3.
 __device__ __forceinline__ float sigmoid(float g)
 {
     const float n = -g * kLog2e;
     const float lost = __builtin_fmaf(-g, kLog2e, -n) - g * kLog2eLow;
     const float p = __builtin_amdgcn_exp2f(n);
-    const float t = fabsf(g) > 80.0f ? p : __builtin_fmaf(p * kLn2, lost, p);
+    const float t = fabsf(n) < 128.0f ? __builtin_fmaf(p * kLn2, lost, p) : p;
     return __builtin_amdgcn_rcpf(1.0f + t);
 }
 
