@@ -22,17 +22,32 @@ namespace {
 // (nontemporal, 5-40 % slower: the second reading then misses).
 constexpr int kGradientPolicy = 2;
 constexpr int kLogitsPolicy = 0;
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLog2eWide = 1.44269504088896340736;
+constexpr float kLog2e = static_cast<float>(kLog2eWide);
+constexpr float kLog2eLow = static_cast<float>(kLog2eWide - static_cast<double>(kLog2e));
 
-// 2^((x - top) log2(e)), the form that also holds at the type's lowest values
-// (where x log2(e) itself is no fp32 number).
-__device__ __forceinline__ float exp_below(float x, float top) { return __builtin_amdgcn_exp2f((x - top) * kLog2e); }
+// e^(x - top) as 2^((x - top) log2(e)), the form that also holds at the type's
+// lowest values (where x log2(e) itself is no fp32 number).  log2(e) is in two
+// parts: what the first one lacks, 1.3e-8 of every exponent, has one sign in
+// all of a row's terms (kl of 1000 x 32003 fp32 was off by 1.5e-7 with one
+// part, is by 4.8e-8, and takes 0.3 to 1.2 % longer).  The rounding of the
+// exponent has no sign and stays.
+__device__ __forceinline__ float exp_below(float x, float top)
+{
+    const float d = x - top;
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kLog2e, d * kLog2eLow));
+}
+
+// The same for a gradient that is rounded to bf16: by the first part alone.
+template <bool kBf16>
+__device__ __forceinline__ float exp_for_store(float x, float top)
+{
+    return kBf16 ? __builtin_amdgcn_exp2f((x - top) * kLog2e) : exp_below(x, top);
+}
 
 // A share of a row: its largest logit and the sum of e^(x - top).  An empty
 // share, or one of -inf logits only, is {-inf, 0}; a NaN or +inf logit makes
-// the sum NaN.  (e is 2^kLog2e throughout, 1 + 1.3e-8 times as steep as the
-// real one; row_values() measures the label's logit in the same units, so that
-// only 1.3e-8 of its distance from the row's mean remains.)
+// the sum NaN.
 struct Share {
     float top;
     double sum;
@@ -53,7 +68,7 @@ __device__ __forceinline__ Share wave_share(float top, float sum)
 __device__ __forceinline__ double rescaled(const Share& s, float top)
 {
     const float base = top == -INFINITY ? 0.0f : top;
-    return s.sum * exp2((static_cast<double>(s.top) - static_cast<double>(base)) * static_cast<double>(kLog2e));
+    return s.sum * exp2((static_cast<double>(s.top) - static_cast<double>(base)) * kLog2eWide);
 }
 
 // Joins the shares of each group of kLanes lanes (a power of two), in a fixed
@@ -87,8 +102,7 @@ __device__ __attribute__((noinline)) RowResult row_values(float top, double sum,
     if (top == -INFINITY && sum == 0.0) return r;  // nothing to choose from: left out
     r.top = top;
     r.label_logit = label_logit;
-    constexpr double kSteep = static_cast<double>(kLog2e) * 0.69314718055994530942;  // 1 + 1.3e-8 less
-    const double logp = (static_cast<double>(label_logit) - static_cast<double>(top)) * kSteep - log(sum);
+    const double logp = (static_cast<double>(label_logit) - static_cast<double>(top)) - log(sum);
     r.logp = static_cast<float>(logp);
     if (!loss_too) return r;
     const double w = weight, adv = advantage;
@@ -266,7 +280,7 @@ struct Units {
         float x[kUnit];
         widen<kBf16>(raw, x);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] = factor * exp_below(x[i], top);
+        for (int i = 0; i < kUnit; ++i) x[i] = factor * exp_for_store<kBf16>(x[i], top);
         store(x, unit);
     }
 };

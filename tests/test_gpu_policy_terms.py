@@ -1,5 +1,5 @@
-"""The policy loss's terms where one of them has no weight: a KL term that is
-only watched."""
+"""The policy loss's terms on their own: a KL term that is only watched, and the
+errors of a row's sum and of the gradient where nothing else hides them."""
 import pytest
 import torch
 
@@ -46,3 +46,56 @@ def test_a_kl_term_without_a_coefficient_is_only_watched(dtype, rows, vocab):
                       s["ref"][others], 0.0)["kl"]
     # d is off by the error of l: at most (6 R + 64) u with a range R below 40, as in the tests of the loss.
     assert ((a[2][others].double() - want).abs() <= (6 * 40 + 64) * U * 3).all()
+
+
+@pytest.mark.parametrize("rows,vocab", KERNELS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_label_far_below_the_others(dtype, rows, vocab):
+    """Every logit 0 but the label's: the sum is a whole number, so l is off by
+    fp64's rounding alone, and the loss, -ratio with an advantage and a weight of
+    1, by its own rounding to fp32, 2^-24 (a steepness off by 1.3e-8 shows as 8e-7)."""
+    far = -60.0 - 4.0 * torch.arange(rows, device=DEV) % 32  # whole numbers of both types; e^l is nothing beside the sum's last bit
+    x = torch.zeros(rows, vocab, dtype=dtype, device=DEV)
+    labels = (torch.arange(rows, device=DEV) * 13) % vocab
+    x[torch.arange(rows, device=DEV), labels] = far.to(dtype)
+    logp = far.double() - torch.log(torch.tensor(vocab - 1.0, dtype=torch.float64, device=DEV))
+    old = logp.float()
+    one, zero = torch.ones(rows, device=DEV), torch.zeros(rows, device=DEV)
+    ws = torch.empty(mps.policy_loss_workspace_bytes(rows, vocab), dtype=torch.uint8, device=DEV)
+    loss, lp, kl = torch.empty(1, device=DEV), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    for i in [0, 1, rows // 2, rows - 1]:
+        weight = zero.clone()
+        weight[i] = 1.0
+        mps.policy_loss(x, labels, old, one, weight, loss, ws, token_logp=lp)
+        want = -torch.exp(logp[i] - old[i].double())
+        assert (loss[0].double() - want).abs() <= 2.0 ** -24 * 1.001, (i, loss.item(), want.item())
+        assert (lp[i].double() - logp[i]).abs() <= logp[i].abs() * 2.0 ** -24 * 1.001
+    # d = ref - l of about 1: kl within its rounding and fp64's
+    mps.policy_loss(x, labels, old, one, one, loss, ws, ref_logp=old + 1, kl_coef=0.1, token_kl=kl)
+    d = (old + 1).double() - logp
+    want = torch.exp(d) - d - 1
+    assert ((kl.double() - want).abs() <= want * 2.0 ** -24 * 1.001).all()
+
+
+@pytest.mark.parametrize("rows,vocab", KERNELS)
+def test_the_gradient_of_unlikely_tokens_has_no_bias(rows, vocab):
+    """fp32 logits 60 to 80 below the largest ones: an exponent's rounding has no
+    sign, so what remains in the mean of the relative errors is at most the power's
+    1 ulp (2^-23), the factor's and the product's rounding (2^-24 each), and the mean of
+    the exponents' own: below 2^-24 |d| / sqrt(n) each way, five times over."""
+    g = gen(vocab + rows)
+    x = torch.zeros(rows, vocab, device=DEV)
+    low = torch.rand(rows, vocab, generator=g, device=DEV) < 0.7
+    low[:, 0] = False
+    x = torch.where(low, torch.empty_like(x).uniform_(-80.0, -60.0, generator=g), x)
+    labels = torch.zeros(rows, dtype=torch.int64, device=DEV)
+    one = torch.ones(rows, device=DEV)
+    l = -torch.log((~low).sum(1).double())  # the unlikely ones' parts are below fp64's last bit
+    d, loss = torch.empty_like(x), torch.empty(1, device=DEV)
+    ws = torch.empty(mps.policy_loss_workspace_bytes(rows, vocab), dtype=torch.uint8, device=DEV)
+    mps.policy_loss(x, labels, l.float(), one, one, loss, ws, dlogits=d)
+    slope = -torch.exp(l - l.float().double())
+    want = -slope[:, None] * torch.exp(x.double() + l[:, None])
+    rel = (d.double() / want - 1)[low]
+    assert (rel.abs() <= 80 * U * 1.5 + 4 * U).all()  # d's product rounded: 80 log2(e) ln 2 u, and as in the bound of the tests of the loss
+    assert rel.mean().abs() <= (2 + 1 + 1) * U + 5 * 80 * U / rel.numel() ** 0.5, rel.mean().item()
