@@ -138,7 +138,8 @@ __global__ __launch_bounds__(kBlock) void act8_swiglu_backward_kernel(
 // so x (or dy) is read once, the weights once per team instead of once per
 // row, and dweight's sums stay in registers over all of a team's rows.  The
 // next row's loads go out before the present row's sum is waited for (except
-// with two units a lane, whose registers they would not fit).
+// with two units a lane, whose registers they would not fit: the fp32 backward
+// with a residual spills 26 of its 128 as it is).
 template <int kThreads>
 struct Team {
     static constexpr int kBlockThreads = kThreads < kBlock ? kBlock : kThreads;
@@ -491,7 +492,11 @@ constexpr int kDweightSplits = 64;   // partial rows of dweight, long rows
 // blocks 52.7, 512 lanes of two units in 256 / 512 blocks 61.9 / 65.4; 8192 x
 // 4096: 512 lanes in 512 blocks 49.8, in 1024 blocks 56.1, 256 lanes of two
 // units in 512 / 1024 blocks 56.7 / 63.0 (more blocks, more partial rows).
-// Forward 8192 x 4096: 26.9, 30.3, 27.8, 27.3 in the same order.
+// Forward 8192 x 4096: 26.9, 30.3, 27.8, 27.3 in the same order.  These widths
+// fill their teams; just above a class's edge lanes idle, and short rows wait for
+// one another: backward 15000 x 576 30 us for bytes worth 12, 4000 x 2176 21.5
+// for 12, 1000 x 8320 22 for 11, and by blocks that read a row twice 400 x 20000
+// 43 for 11 (forward 19, 13, 11 and 16 for 7 each).
 template <class F>
 bool with_team(int64_t cols, F&& f)
 {

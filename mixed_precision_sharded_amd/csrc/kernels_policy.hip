@@ -5,9 +5,9 @@
 // pass with a running maximum; one value per row (ratio, clip, KL term, the
 // slope d loss / d l) is computed in fp64, and the gradient is slope * (onehot
 // - softmax).  The logits are read and the gradient written once, 4 bytes a
-// logit in bf16, so many rows are bound by memory: 8192 x 128256 bf16 790 us
-// (5.3 TB/s), 4000 x 32003 fp32 205 us (5.0 TB/s).  Few rows are bound by two
-// launches that wait for one another: 24 x 128256 bf16 12.9 us.
+// logit in bf16, so many rows are bound by memory: 8192 x 128256 bf16 791 us
+// (5.3 TB/s), 4000 x 32003 fp32 216 us (4.7 TB/s).  Few rows are bound by two
+// launches that wait for one another: 24 x 128256 bf16 13 us.
 #include <hip/hip_runtime.h>
 
 #include "rows.h"
@@ -398,7 +398,8 @@ __global__ __launch_bounds__(kBlock) void policy_block_kernel(PolicyArgs a, doub
 // place, so that no barrier is needed) for the next kLds, and only what lies
 // behind is read again.  A register that has given its gradient asks for the
 // next row's unit at once, so half of the next row is on its way while this
-// one is written.  Rows of at least kThreads * kRegs units of eight.
+// one is written.  Rows of at least kThreads * kRegs units of eight.  (Of 1024
+// threads each has 128 registers, and spills 12 of them in bf16, 23 in fp32.)
 template <bool kBf16, int kThreads, int kRegs, int kLds>
 __global__ __launch_bounds__(kThreads) void policy_kept_kernel(PolicyArgs a, double* losses)
 {
@@ -595,19 +596,28 @@ __global__ __launch_bounds__(kBlock) void policy_total_kernel(const double* valu
     if (threadIdx.x == 0) *loss = static_cast<float>(s);
 }
 
-// Which kernel takes a call, by rows and vocabulary (measured with all of
-// them forced on the same calls, us):
-//   - up to kWaveVocab logits a row is a wavefront's: 8000 x 5000 bf16 42.6
-//     against 49.4 with a block each, 30000 x 1000 39.8 against 102.6;
+// Which kernel takes a call, by rows and vocabulary (measured with the others
+// forced on the same calls, us, over more than 1 GB of inputs in turn; bf16
+// where nothing else is said):
+//   - up to kWaveVocab logits a row is a wavefront's: 8000 x 5000 52 against 69
+//     with a block each, 8000 x 2000 32 against 44, 30000 x 1000 49 against
+//     127.  The rule does not look at the rows, and loses where they do not
+//     fill the chip, sixteen to a block: 16 x 8000 38 against 12, 1000 x 8000
+//     45 against 15, 1000 x 2000 23 against 13 (fp32 4000 x 5000 52 against 47);
 //   - above, a block's of 256 threads that reads it twice, up to kBlockVocab
-//     logits: 2000 x 9000 bf16 20.3 (28 when it was kept), 1000 x 12000 fp32
-//     23.9 (25);
-//   - above that, kept by a block of 512 or 1024: 1000 x 32003 bf16 27.4
-//     against 34.6 read twice, 8192 x 128256 bf16 790 against 1077, 2000 x
-//     65000 fp32 218 against 275, 1000 x 32003 fp32 49.5 against 56.5;
+//     logits: 2000 x 9000 24 against 47 by wavefronts and 26 when the 256 keep
+//     it, 8000 x 9000 77, 87 and 80.  Keeping is ahead from about 10000 on:
+//     8000 x 12000 98 against 90, 2000 x 16000 42 against 35;
+//   - above that, kept by a block of 512 or 1024: 1000 x 32003 35 against 43
+//     read twice, 4000 x 32003 123 against 149, 8192 x 128256 791 against 1079,
+//     fp32 2000 x 65000 227 against 263, 1000 x 32003 59 against 66; but 2000 x
+//     20000 46 and 46, fp32 85 against 78;
 //   - up to kFewRows rows of more than kShareVocab logits, blocks share a row:
-//     24 x 128256 bf16 12.9 against 19.1 kept, 64 x 200000 15.9 against 29.1,
-//     24 x 50257 12.5 against 13.7; but 128 x 128256 22.6 against 20.1.
+//     24 x 128256 14.9 against 20.9 kept, 64 x 200000 19.0 against 33.4, 24 x
+//     50257 12.0 against 15.0, fp32 64 x 128256 22.7 against 29.7; 24 x 32000
+//     12 either way.  kFewRows is a wavefront's lanes (policy_rows_kernel sums
+//     the loss a row per lane) and not where the two sides meet: 64 x 128256
+//     takes 16.4, 65 rows, kept, 22.4.
 constexpr int64_t kWaveVocab = 8192;
 constexpr int64_t kBlockVocab = 16384;
 constexpr int64_t kFewRows = 64;

@@ -1,10 +1,12 @@
 // gfx950 kernel of the weight gradient from 8-bit activations:
 //     dw[n, k] = sum over t of dy[t, n] * x[t, k]
 // on the matrix cores.  An E4M3 code has four significant bits and its scale
-// is a power of two, so a kept value is a bf16 value exactly and its product
+// is a power of two, so a kept value of 2^-126 or more is a bf16 value exactly
+// (a smaller one rounds to the bits that bf16 has left there) and its product
 // with a bf16 gradient has at most 12 significant bits: bf16 operands with
-// fp32 sums lose nothing on the way in.  fp32 gradients are split into three
-// bf16 parts of eight bits each, whose sum they are.
+// fp32 sums lose nothing else on the way in.  fp32 gradients are split into
+// three bf16 parts of eight bits each, whose sum they are down to 2^-133, where
+// bf16 ends.
 //
 // Both operands lie with the summed index t as their slow one, while a lane
 // of the matrix instruction wants eight t of one column.  Tiles are staged in
@@ -14,7 +16,9 @@
 // Large products are bound by the matrix instructions (8192 x 4096 x 4096 bf16
 // 208 us, 1320 TF/s, their pipes busy 75 % of the cycles; fp32 594 us, three
 // products at 1390 TF/s; a chip under this load lowers its clock), small ones
-// by the stages' waits and the launch (fp32 777 x 1000 x 2051 25.6 us).
+// by the stages' waits and the launch (fp32 777 x 1000 x 2051 25.6 us).  Adding
+// to what dw holds is a load, a sum and a store per value behind the product:
+// 8192 x 4096 x 4096 305 us into fp32, 267 into bf16.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -69,7 +73,7 @@ __device__ __forceinline__ bf16x8 read_operand(const char* tile, int t0, int col
 
 // Eight fp32 values as three bf16 parts each: the leading eight bits, the next
 // eight, the rest (cut off, not rounded, so each remainder is exact and no
-// part overflows).  A value that is not finite is its own first part: the
+// part overflows; bits below 2^-133 are lost).  A value that is not finite is its own first part: the
 // remainder of an infinity is a NaN, and is set to zero, as a NaN's is, whose
 // quiet bit keeps it one in the upper half.
 __device__ __forceinline__ void split3(const Raw8<false>& raw, u32x4 (&part)[3])
@@ -282,7 +286,8 @@ __global__ __launch_bounds__(kBlock, 2) void weight_grad_kernel(Matrix dy, Codes
 // chunk of a row reaches into the next row, which is harmless except in the
 // very last one: that token is left out of the stages and added to the sums
 // at the end, and the rows behind it are cleared in registers (8192 x 4095 x
-// 4096 bf16 240 us, fp32 630).
+// 4096 bf16 240 us, fp32 630; this form spills 178 registers, the aligned one at
+// most 6).
 
 constexpr int kWideTile = 256;
 constexpr int kWideRow = kWideTile * 2;  // bytes of a staged row
