@@ -180,7 +180,8 @@ int act8_weight_grad(const void* d_dy, mps_dtype dy_dtype, int64_t dy_stride,
  * when its label is outside [0, vocab) or its weight is 0, and so is a row
  * whose logits are all -inf.  Single logits of -inf are tokens the
  * vocabulary does not offer (a label among them has l = -inf: a ratio of 0
- * and an infinite KL term); a NaN or +inf logit makes its row NaN.
+ * and an infinite KL term); a NaN or +inf logit makes its row NaN (in the loss
+ * where its advantage or the KL term counts).
  *
  *   d_logits, logits_dtype, logits_stride : [rows, vocab].
  *   d_labels     : int64 [rows].
