@@ -55,13 +55,14 @@ constexpr double kLog2eWide = 1.44269504088896340736;
 constexpr float kLog2e = static_cast<float>(kLog2eWide);
 constexpr float kLog2eLow = static_cast<float>(kLog2eWide - static_cast<double>(kLog2e));
 
-// e^(x - top), log2(e) in two parts (the error of one has the same sign in all
-// of a row's terms).
-__device__ __forceinline__ float exp_below(float x, float top)
+// e^(x - top) and its logarithm to base 2, log2(e) in two parts (the error of
+// one has the same sign in all of a row's terms).
+__device__ __forceinline__ float log2_below(float x, float top)
 {
     const float d = x - top;
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kLog2e, d * kLog2eLow));
+    return __builtin_fmaf(d, kLog2e, d * kLog2eLow);
 }
+__device__ __forceinline__ float exp_below(float x, float top) { return __builtin_amdgcn_exp2f(log2_below(x, top)); }
 
 // ------------------------------------------------------------ the product ---
 
@@ -466,7 +467,10 @@ struct Sixteen {
 // For each token of the tile: the largest of this wavefront's 128 logits, the
 // sum of e^(x - largest), and its label's logit where it is among them.
 // kLogits: also leaves the logits, rows of tokens, for a later pass; rows that are none are stored outside the buffer, which
-// drops them without a branch.  kExp: puts e^(x - largest) in fp16 (11 bits of at most 1) into LDS as tile_row_at says.
+// drops them without a branch.  kExp: puts e^(x - largest) in 16 bits into LDS as tile_row_at says: minus its logarithm to
+// base 2 in steps of 1 / kLogSteps.  So every one of them down to 2^-64 of the largest is kept to 2^-11 ln 2 = 3.4e-4 of
+// itself (fp16 keeps the large ones to 4.9e-4, and of what is beside a label with nearly all of its row it loses bits below
+// 2^-14 and everything below 2^-25); smaller ones, the largest code, are zeros.
 enum class Keep { kNone, kLogits, kExp };
 
 // Where four entries from `entry` on, of a tile's row t, lie in LDS: rows of 256 entries of 16 bits, whose 16-byte chunks
@@ -486,12 +490,20 @@ __device__ __forceinline__ void store_tile_rows(const char* lds, const Target& t
     }
 }
 
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+constexpr float kLogSteps = 1024.0f;
+constexpr uint32_t kLogMost = 65535;  // of what the logarithms are held to
 
-__device__ __forceinline__ uint32_t f16_pack2(float a, float b)
+// Two logarithms, at most 0, as codes: to the nearest step, both ends held (a NaN gives 0, but then its row's sum is one).
+__device__ __forceinline__ uint32_t log_pack2(float a, float b)
 {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+    constexpr float kUnits = -kLogSteps / static_cast<float>(kLogMost);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(a * kUnits, b * kUnits));
+}
+
+// The power of two that a code stands for, under 2^top.
+__device__ __forceinline__ float log_value(uint32_t code, float top)
+{
+    return code == kLogMost ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(static_cast<float>(code), -1.0f / kLogSteps, top));
 }
 
 template <bool kEdge, Keep kKeep, int kI, int kJ>
@@ -520,17 +532,17 @@ __device__ __forceinline__ void stats_of(const f32x16 (&acc)[kI][kJ], const Targ
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
             const Sixteen v(acc[i][j]);
-            float e[16];
+            float log[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                e[r] = exp_below(!kEdge || i * kFrag + row_of(r, lane) < there ? v.x[r] : -INFINITY, under);
-                part[r % 4] += e[r];
+                log[r] = log2_below(!kEdge || i * kFrag + row_of(r, lane) < there ? v.x[r] : -INFINITY, under);
+                part[r % 4] += __builtin_amdgcn_exp2f(log[r]);
             }
             if (kKeep == Keep::kExp) {
                 const int wave = threadIdx.x / kWave, t = wave % 2 * 128 + j * kFrag + lane % 32;
 #pragma unroll
                 for (int r = 0; r < 16; r += 4) {
-                    const u32x2 w = {f16_pack2(e[r], e[r + 1]), f16_pack2(e[r + 2], e[r + 3])};
+                    const u32x2 w = {log_pack2(log[r], log[r + 1]), log_pack2(log[r + 2], log[r + 3])};
                     *reinterpret_cast<u32x2*>(lds + tile_row_at(t, wave / 2 * 128 + i * kFrag + row_of(r, lane))) = w;
                 }
             }
@@ -1417,12 +1429,15 @@ __global__ __launch_bounds__(kBlock) void scale_kernel(const float2* stats, int6
     for (RowWalk w(per_row); w.row < live; w.next()) {
         const int64_t c = static_cast<int64_t>(w.col) * kUnit, label = s.label[w.row] - first - c;
         u32x4* at = reinterpret_cast<u32x4*>(g + (w.row * stride + c) * 2);
-        const f16x8 e = __builtin_bit_cast(f16x8, *at);
+        const u32x4 codes = *at;
         const float top = s.top[w.row], factor = s.factor[w.row];
-        const float scale = factor * exp_below(stats[c / 128 * padded + w.row].x, top);
+        const float under = log2_below(stats[c / 128 * padded + w.row].x, top);
         float x[kUnit];
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] = c + i < size ? static_cast<float>(e[i]) * scale : 0.0f;
+        for (int i = 0; i < kUnit; ++i) {
+            const uint32_t code = i % 2 ? codes[i / 2] >> 16 : codes[i / 2] & 0xffffu;
+            x[i] = c + i < size ? factor * log_value(code, under) : 0.0f;
+        }
         if (label >= 0 && label < kUnit) {
             const float at_label = grad_at<1>(s.label_logit[w.row], top, factor) - s.slope[w.row];
 #pragma unroll

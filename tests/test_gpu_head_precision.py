@@ -1,0 +1,32 @@
+"""linear_cross_entropy's bf16 g, entry by entry, against the bounds of
+head_precision: relative to the entry, not to its row."""
+import pytest
+import torch
+
+import head_precision as hp
+import mixed_precision_sharded_amd as mps
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def gradients(hidden, weight, labels, c, dw_type):
+    (tokens, cols), vocab = hidden.shape, len(weight)
+    ws = torch.empty(mps.linear_cross_entropy_workspace_bytes(tokens, vocab, cols, BF16), dtype=torch.uint8, device=DEV).fill_(255)
+    loss, dh = torch.empty(1, device=DEV), torch.empty_like(hidden)
+    dw = torch.empty(vocab, cols, dtype=dw_type, device=DEV)
+    mps.linear_cross_entropy(hidden, weight, labels, c, loss, ws, dhidden=dh, dweight=dw)
+    return dh, dw
+
+
+@pytest.mark.parametrize("gap", [12.0, 18.0, 24.0, 34.0])
+@pytest.mark.parametrize("tokens,vocab,cols", [(24, 1500, 64), (300, 1500, 64), (300, 10007, 64), (300, 10007, 72), (1100, 5000, 64)])
+def test_entries_far_below_the_label(tokens, vocab, cols, gap):
+    """Rows that are sure of their label: what is left for the entries beside it keeps its bits."""
+    p = hp.problem(tokens, vocab, cols, gap, device=DEV)
+    r = hp.exact(*p)
+    for dw_type in (F32, BF16):
+        dh, dw = gradients(*p, dw_type)
+        assert hp.outside(dw, r["dw"], r["dw_off"]) == 0
+        assert hp.outside(dh, r["dh"], r["dh_off"]) == 0
