@@ -30,3 +30,18 @@ def test_entries_far_below_the_label(tokens, vocab, cols, gap):
         dh, dw = gradients(*p, dw_type)
         assert hp.outside(dw, r["dw"], r["dw_off"]) == 0
         assert hp.outside(dh, r["dh"], r["dh_off"]) == 0
+
+
+@pytest.mark.parametrize("tokens,vocab,cols", [(1, 1000, 64), (24, 2000, 64), (24, 2000, 72), (32, 3001, 200), (40, 2000, 72), (60, 2000, 64),
+                                               (200, 4000, 64), (200, 4000, 72), (600, 9001, 64), (600, 20000, 72), (1100, 30011, 128)])
+def test_g_at_the_label_has_16_bits(tokens, vocab, cols):
+    """Few tokens and more, logits that stay and exponentials that do, weights as they lie and packed."""
+    p = hp.problem(tokens, vocab, cols, device=DEV)
+    r = hp.exact(*p)
+    for dw_type in (F32, BF16):
+        dh, dw = gradients(*p, dw_type)
+        assert hp.outside(dw, r["dw"], r["dw_off"]) == 0
+        assert hp.outside(dh, r["dh"], r["dh_off"]) == 0
+    # The bound is one that g without its correction does not keep.
+    dh, dw = hp.simulate(*p, correction=0.0)
+    assert hp.outside(dw, r["dw"], r["dw_off"]) > 0
