@@ -11,8 +11,8 @@
 // of the vocabulary the same product is made again, its tiles turned into g in
 // a workspace, and g goes into the two gradients' products.  The last piece of
 // the first pass leaves its exponentials in that workspace, so that its logits
-// are made once (8192 x 128256 x 4096, where that is all of it: 19.8 ms; 22.2
-// with half of it, 25.3 with none).
+// are made once (8192 x 128256 x 4096, where that is half of them: 22.1 ms; 25.3
+// with none).
 // What a bf16 g loses at the label, where it is largest, is added again: to
 // dh with the label's row of w, to dw as a few more stages of the product of
 // the tile that holds the label (rows of neighbouring labels lie together).
@@ -1485,9 +1485,11 @@ __global__ __launch_bounds__(kBlock) void hidden_kernel(const float* partials, i
 
 // ------------------------------------------------------------- the plan ---
 
-// Of a piece's g, with fp32 operands and few tokens its logits too.  What is behind it is made twice: 8192 x 128256 x 4096,
-// 2.1 GB of bf16, takes 19.8 ms; with 1 GB 22.2.  Less than a hundredth of the card's memory.
-constexpr int64_t kPieceBytes = 2ll << 30;
+// Of a piece: its g, with fp32 operands and few tokens its logits too, and of the weight what is packed.  Half of what all
+// logits would take in the operands' type, so that the call stays an alternative to making them; at least kLeastPieceBytes,
+// where the logits are not worth the time, and at most kMostPieceBytes.  What is behind it is made twice: 8192 x 128256 x
+// 4096 (2.1 GB of logits) takes 22.1 ms, with all of it kept 19.5; 8192 x 32000 x 4096 (0.5 GB, all kept) 4.9, with half 5.9.
+constexpr int64_t kLeastPieceBytes = 512ll << 20, kMostPieceBytes = 2ll << 30;
 constexpr int64_t kPackedBytes = 512ll << 20; // of a packed piece of the weight
 constexpr int64_t kStatBytes = 128ll << 20;   // of the statistics of a part of the first pass
 constexpr int64_t kLeastPiece = 2048;
@@ -1538,7 +1540,12 @@ Plan plan_of(int64_t tokens, int64_t vocab, int64_t cols, bool bf16, bool packed
     const int64_t all = up(vocab, kTile), by_stats = within(all, kStatBytes, up(16 * p.rows, kTile) / kTile);
     int64_t most = all;
     if (p.packed) most = within(most, kPackedBytes, 2 * p.parts * p.cols);
-    if (gradients) most = within(most < kMostPiece ? most : kMostPiece, kPieceBytes, (2 * p.parts + (p.logits ? 4 : 0)) * p.rows);
+    if (gradients) {
+        const int64_t half = p.rows * all * (bf16 ? 1 : 2);  // bytes
+        const int64_t room = half < kLeastPieceBytes ? kLeastPieceBytes : (half < kMostPieceBytes ? half : kMostPieceBytes);
+        const int64_t of_entry = (2 * p.parts + (p.logits ? 4 : 0)) * p.rows + (p.packed ? 2 * p.parts * p.cols : 0);
+        most = within(most < kMostPiece ? most : kMostPiece, room, of_entry);
+    }
     if (most > by_stats && !gradients) most = by_stats;
     p.last = all - most;
     p.others = (p.last + most - 1) / most;
