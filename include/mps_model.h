@@ -121,15 +121,15 @@ int dropout(const void* d_x, mps_dtype dtype, int64_t x_stride, int64_t rows, in
  *   d_token_logp   : fp32 [tokens], l, or NULL.
  *   tokens <= 2^24, features <= 2^20.
  * The workspace: without gradients the packed hidden states (2 bytes a value,
- * fp32: 6), up to 128 MB of statistics, and up to 512 MB for a piece of a weight
- * that cannot be read as it lies; with gradients also an fp32 dhidden (several,
- * where it has few tiles), and for a piece's g and what is packed of its weight
- * half of what the logits would take in the operands' type, but up to 512 MB
- * where that is more and 2 GB where that is less (2048 entries at least).  A
- * bf16 weight can be read as it lies where features are a multiple of 64, rows
- * start at 16 bytes and the stride is at most 2^21; up to 64 tokens any weight
- * can, and without gradients where tokens times vocab, each rounded up to 256,
- * is at most 2^22.
+ * fp32: 6), up to 128 MB of statistics (128 bytes a token where that is more),
+ * and up to 512 MB for a piece of a weight that cannot be read as it lies; with
+ * gradients also an fp32 dhidden (several, where it has few tiles), and for a
+ * piece's g and what is packed of its weight half of what the logits would take
+ * in the operands' type, but up to 512 MB where that is more and 2 GB where that
+ * is less (2048 entries at least).  A bf16 weight can be read as it lies where
+ * features are a multiple of 64, rows start at 16 bytes and the stride is at
+ * most 2^21; up to 64 tokens any weight can, and without gradients where tokens
+ * times vocab, each rounded up to 256, is at most 2^22.
  */
 size_t linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t features,
                                             mps_dtype dtype, int gradients);

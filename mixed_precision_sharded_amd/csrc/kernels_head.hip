@@ -1537,7 +1537,8 @@ Plan plan_of(int64_t tokens, int64_t vocab, int64_t cols, bool bf16, bool packed
         const int64_t n = bytes / of_entry / kTile * kTile;
         return n < kLeastPiece ? (most < kLeastPiece ? most : kLeastPiece) : (n < most ? n : most);
     };
-    const int64_t all = up(vocab, kTile), by_stats = within(all, kStatBytes, up(16 * p.rows, kTile) / kTile);
+    // A float2 a row and stretch, two stretches a tile, four of the small ones.
+    const int64_t all = up(vocab, kTile), by_stats = within(all, kStatBytes, (p.small ? 32 : 16) * p.rows / kTile);
     int64_t most = all;
     if (p.packed) most = within(most, kPackedBytes, 2 * p.parts * p.cols);
     if (gradients) {
