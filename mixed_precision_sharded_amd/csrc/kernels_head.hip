@@ -1542,7 +1542,7 @@ Plan plan_of(int64_t tokens, int64_t vocab, int64_t cols, bool bf16, bool packed
     int64_t most = all;
     if (p.packed) most = within(most, kPackedBytes, 2 * p.parts * p.cols);
     if (gradients) {
-        const int64_t half = p.rows * all * (bf16 ? 1 : 2);  // bytes
+        const int64_t half = tokens * vocab * (bf16 ? 1 : 2);  // bytes
         const int64_t room = half < kLeastPieceBytes ? kLeastPieceBytes : (half < kMostPieceBytes ? half : kMostPieceBytes);
         const int64_t of_entry = (2 * p.parts + (p.logits ? 4 : 0)) * p.rows + (p.packed ? 2 * p.parts * p.cols : 0);
         most = within(most < kMostPiece ? most : kMostPiece, room, of_entry);
