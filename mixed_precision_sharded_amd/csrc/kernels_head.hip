@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "model_kernels.h"
+#include "parts.h"
 #include "rows.h"
 
 namespace mps {
@@ -107,14 +108,6 @@ struct Target {
     int64_t out_stride, out_plane;  // elements
     bool accumulate, bf16;
 };
-
-// Parts that are multiplied: those whose product can reach 2^-16 of the largest
-// (the others are at most 2^-24 of it each), the smallest first: the sums of
-// the small ones then round at their own size, and fp32 logits are half as far
-// off as with the largest first.
-constexpr int kPairs = 6;
-__device__ __forceinline__ int part_a(int pair) { return (0x001012 >> (4 * pair)) & 0xf; }
-__device__ __forceinline__ int part_b(int pair) { return (0x010210 >> (4 * pair)) & 0xf; }
 
 // The three bf16 parts of eight fp32 values: each the nearest to what is left,
 // and together all of their 24 bits.  The first is held to the largest finite
