@@ -107,7 +107,9 @@ int dropout(const void* d_x, mps_dtype dtype, int64_t x_stride, int64_t rows, in
  * A row is left out (l 0, no part in the loss or dweight, zeros in dhidden;
  * nothing of its hidden state is read) when its label is outside [0, vocab) or
  * its weight is 0; rows that are left out cost next to nothing.  A value that
- * is not finite makes the rows and gradients that it reaches NaN.
+ * is not finite makes the rows and gradients that it reaches NaN; but with bf16
+ * operands, whose products are made as they are, an entry with a logit of minus
+ * infinity has the probability 0 and leaves l of its row finite.
  *
  *   dtype          : of hidden, weight and dhidden.
  *   d_hidden       : [tokens, features].      d_weight : [vocab, features].
