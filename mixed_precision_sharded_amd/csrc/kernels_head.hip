@@ -33,6 +33,7 @@
 
 #include <type_traits>
 
+#include "mfma.h"
 #include "model_kernels.h"
 #include "parts.h"
 #include "rows.h"
@@ -40,14 +41,8 @@
 namespace mps {
 namespace {
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr int kTile = 256;       // of m and of n
 constexpr int kStage = 64;       // of k
-constexpr int kFrag = 32;        // rows and columns of one matrix instruction
 constexpr int kOperand = kTile * kStage * 2;  // bytes of a staged operand
 constexpr int kB = 2 * kOperand;              // A: two stages, then B: two stages
 constexpr int kGroup = 8;        // tiles of n in a patch of neighbouring ones
@@ -188,10 +183,7 @@ struct Staged {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const char* p = lds + read_at[i] + buf * kOperand + step * 16 * 512;
-                const bf16x4 lo = __builtin_bit_cast(
-                    bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
-                const bf16x4 hi = __builtin_bit_cast(
-                    bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * 512)));
+                const bf16x4 lo = load_transposed(p), hi = load_transposed(p + 4 * 512);
                 v[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         } else {
@@ -202,32 +194,6 @@ struct Staged {
         }
     }
 };
-
-// The order of a step's instructions: its LDS reads behind the first eight
-// matrix instructions, the writes behind the next, the loads from memory
-// behind the first ones.  A stage of 64 matrix instructions of 32 cycles takes
-// 2500 cycles.
-template <int kReads, int kWrites, int kLoads>
-__device__ __forceinline__ void order_step()
-{
-    constexpr int kMfma = 0x008, kVmemRead = 0x020, kLdsRead = 0x100, kLdsWrite = 0x200;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-        if (i < 8) {
-            if constexpr (kReads == 16) __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
-            else if constexpr (kReads == 12) {
-                if (i % 2) __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
-                else __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-            }
-            else __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-        } else if (i - 8 < kWrites) {
-            __builtin_amdgcn_sched_group_barrier(kLdsWrite, 1, 0);
-        }
-        if (i < kLoads) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-}
 
 template <Kind kKind, int kParts>
 __device__ void finish_tile(const f32x16 (&acc)[4][4], char* lds, const Product& p, const Target& to, int64_t m0, int64_t n0,
@@ -366,7 +332,7 @@ __device__ __forceinline__ void product(Product p, const Target& to, char* lds, 
     a.read(av[0], lds, 0, 0);
     b.read(bv[0], lds, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    // A stage: four steps of 16 matrix instructions.  A step reads the operands of the next one; the first three put the
+    // A stage: four steps of 16 matrix instructions of 32 cycles, 2500 cycles in all.  A step reads the operands of the next one; the first three put the
     // next stage, which is in registers, into LDS, and ask for the one after it into the registers that they freed.
     constexpr int kReads = Staged<kASlow>::kReads + Staged<kBSlow>::kReads;
     auto stage = [&](int buf) __attribute__((always_inline)) {
@@ -921,25 +887,6 @@ __global__ __launch_bounds__(kBlock, 2) void few_stats_f32_kernel(Product p, Mat
     finish_few<kJ>(acc, lds, p.m, m0, to, live);
 }
 
-// Byte of 16-byte chunk `chunk` of row t in a tile of rows of kCols bf16, spread like Staged's slow tiles.
-template <int kCols>
-__device__ __forceinline__ uint32_t chunk_at(int t, int chunk)
-{
-    return t * kCols * 2 + ((kCols == 64 ? chunk ^ ((t & 2) << 1) : chunk ^ ((t & 3) << 2)) << 4);
-}
-
-// The operand of a matrix instruction: columns col0 .. col0 + 31, rows t0 .. t0 + 15.
-template <int kCols>
-__device__ __forceinline__ bf16x8 read_slow(const char* tile, int t0, int col0, int lane)
-{
-    const int t = t0 + lane / 32 * 8 + lane % 16 / 4, c = col0 + lane % 32 / 16 * 16 + lane % 4 * 4;
-    const char* p = tile + chunk_at<kCols>(t, c / 8) + c % 8 * 2;
-    const char* q = tile + chunk_at<kCols>(t + 4, c / 8) + c % 8 * 2;
-    const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
-    const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)q));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // kWeight for at most kT tokens: one or two steps of the matrix instruction a
 // tile, so that the tile's way to memory is all there is.  A block has 256
 // features (fp32: 128), whose operands stay in registers, and takes one tile of
@@ -1002,7 +949,7 @@ __global__ __launch_bounds__(kBlock, kT == 32 && !kAccumulate ? (kParts == 1 ? (
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) b[part][step][j] = read_slow<kCols>(rest + part * kH, step * 16, wave * (kCols / 4) + j * kFrag, lane);
+            for (int j = 0; j < kJ; ++j) b[part][step][j] = read_operand<kCols>(rest + part * kH, step * 16, wave * (kCols / 4) + j * kFrag, lane);
         }
     }
 #pragma unroll 1
@@ -1032,7 +979,7 @@ __global__ __launch_bounds__(kBlock, kT == 32 && !kAccumulate ? (kParts == 1 ? (
             for (int pair = kFirst; pair < kPairs; ++pair) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const bf16x8 a = read_slow<64>(lds + part_a(pair) * kG, step * 16, i * kFrag, lane);
+                    const bf16x8 a = read_operand<64>(lds + part_a(pair) * kG, step * 16, i * kFrag, lane);
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[part_b(pair)][step][j], acc[i][j], 0, 0, 0);
                 }
@@ -1040,7 +987,7 @@ __global__ __launch_bounds__(kBlock, kT == 32 && !kAccumulate ? (kParts == 1 ? (
             if (lost_too) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const bf16x8 a = read_slow<64>(lds + kG, step * 16, i * kFrag, lane);
+                    const bf16x8 a = read_operand<64>(lds + kG, step * 16, i * kFrag, lane);
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[0][step][j], acc[i][j], 0, 0, 0);
                 }
@@ -1198,7 +1145,7 @@ __global__ __launch_bounds__(kBlock, 2) void few_hidden_any_kernel(Product p, Ma
             bf16x8 a[kParts][kJ], b[kParts];
 #pragma unroll
             for (int q = 0; q < kParts; ++q) {
-                b[q] = read_slow<128>(lds + kParts * kA + q * kW, step * 16, wave * 32, lane);
+                b[q] = read_operand<128>(lds + kParts * kA + q * kW, step * 16, wave * 32, lane);
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) a[q][j] = *reinterpret_cast<const bf16x8*>(lds + q * kA + j * 4096 + at);
             }

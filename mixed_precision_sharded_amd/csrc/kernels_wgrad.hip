@@ -23,53 +23,14 @@
 
 #include <type_traits>
 
+#include "mfma.h"
 #include "rows.h"
 #include "train_kernels.h"
 
 namespace mps {
 namespace {
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr int kStageBf16 = 64, kStageF32 = 32;  // t per stage of the tiles of 128 and 64
-constexpr int kFrag = 32;    // rows and columns of one matrix instruction
-
-// Byte offset in a staged tile [t][kCols] of bf16 of the 16-byte chunk
-// `chunk` of row t.  A transposing load reads 32 bytes from each of four
-// consecutive rows per 16 lanes; the exclusive-or sends the four rows to
-// different banks (rows of 64 columns lie two to the banks' 256 bytes).
-template <int kCols>
-__device__ __forceinline__ uint32_t chunk_at(int t, int chunk)
-{
-    const int mixed = kCols == 64 ? chunk ^ ((t & 2) << 1) : chunk ^ ((t & 3) << 2);
-    return static_cast<uint32_t>(t * kCols * 2 + (mixed << 4));
-}
-
-// Four t (t0 .. t0 + 3) of column `col` for each lane of a group of 16, whose
-// lanes hold 16 consecutive columns from col0 on.
-template <int kCols>
-__device__ __forceinline__ bf16x4 read_transposed(const char* tile, int t0, int col0, int lane16)
-{
-    const int t = t0 + lane16 / 4;
-    const int col = col0 + lane16 % 4 * 4;
-    const char* p = tile + chunk_at<kCols>(t, col / 8) + (col % 8) * 2;
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                          (__attribute__((address_space(3))) s16x4*)p));
-}
-
-// The operand of one matrix instruction: columns col0 .. col0 + 31 (lane %
-// 32), t0 + 8 * (lane / 32) .. + 7.
-template <int kCols>
-__device__ __forceinline__ bf16x8 read_operand(const char* tile, int t0, int col0, int lane)
-{
-    const int t = t0 + lane / 32 * 8, c = col0 + lane % 32 / 16 * 16;
-    const bf16x4 lo = read_transposed<kCols>(tile, t, c, lane % 16);
-    const bf16x4 hi = read_transposed<kCols>(tile, t + 4, c, lane % 16);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
 
 // Eight fp32 values as three bf16 parts each: the leading eight bits, the next
 // eight, the rest (cut off, not rounded, so each remainder is exact and no
@@ -296,26 +257,6 @@ constexpr int kWideBf16 = 64, kWideF32 = 32;  // t per stage
 __device__ __forceinline__ uint32_t wide_chunk_at(int t, int chunk)
 {
     return static_cast<uint32_t>(t * kWideRow + ((chunk ^ ((t & 3) << 2)) << 4));
-}
-
-// The order of a step's instructions: its LDS reads behind the first eight
-// matrix instructions (two behind each if there are sixteen) and a write behind each of the next, with a load
-// from memory behind each of the first (asked for one by one, the compiler
-// gathers them before or behind the matrix instructions, which then wait:
-// 267 instead of 220 us for 8192 x 4096 x 4096; one read behind each of the
-// sixteen, with the writes last, took 238).
-template <int kReads, int kWrites, int kLoads>
-__device__ __forceinline__ void order_step()
-{
-    constexpr int kMfma = 0x008, kVmemRead = 0x020, kLdsRead = 0x100, kLdsWrite = 0x200;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-        if (i < 8) __builtin_amdgcn_sched_group_barrier(kLdsRead, kReads / 8, 0);
-        else if (i - 8 < kWrites) __builtin_amdgcn_sched_group_barrier(kLdsWrite, 1, 0);
-        if (i < kLoads) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
 }
 
 // A thread's share of a stage on its way from memory.
