@@ -179,8 +179,9 @@ static_assert(kSortThreads == 2 * kBins, "two threads a digit");
 
 // At most kRankMost tokens, in one launch: a token's place is the number of tokens before it, counted over all keys in LDS.
 // A block places kRankTokens, each with kRankTokens groups of threads that have a share of the keys; and it has the flags of
-// kRankFlags rows of the table.  The gradient of 777 x 2051 into 32003 rows takes 69 us with it, 75 with digits sorted by
-// one block; that of 8192 x 4096 into 128256 rows 400, 408 with two launches a digit.
+// kRankFlags rows of the table.  The gradient of 256 features into 32003 rows, in us with it and with two launches a digit:
+// 512 tokens 22 and 33, 2048 25 and 35, 4096 28 and 37, 8192 33 and 39, 10000 41 and 40, 16384 50 and 38 (with LDS for as
+// many keys).
 constexpr int kRankMost = 8192, kRankTokens = 32, kRankFlags = 4096;
 
 __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortPass p)

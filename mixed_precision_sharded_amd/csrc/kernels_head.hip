@@ -332,8 +332,9 @@ __device__ __forceinline__ void product(Product p, const Target& to, char* lds, 
     a.read(av[0], lds, 0, 0);
     b.read(bv[0], lds, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    // A stage: four steps of 16 matrix instructions of 32 cycles, 2500 cycles in all.  A step reads the operands of the next one; the first three put the
-    // next stage, which is in registers, into LDS, and ask for the one after it into the registers that they freed.
+    // A stage: four steps of 16 matrix instructions of 32 cycles, 2500 cycles in all.  A step reads the operands of the next
+    // one; the first three put the next stage, which is in registers, into LDS, and ask for the one after it into the
+    // registers that they freed.
     constexpr int kReads = Staged<kASlow>::kReads + Staged<kBSlow>::kReads;
     auto stage = [&](int buf) __attribute__((always_inline)) {
         a.read(av[1], lds, buf, 1);
@@ -531,7 +532,8 @@ __device__ __forceinline__ void stats_of(const f32x16 (&acc)[kI][kJ], const Targ
     }
 }
 
-// g at a logit.  For bf16 with the first part of log2(e) alone.
+// g at a logit.  For bf16 with the first part of log2(e) alone: 1.3e-8 of the value for each that the logit lies below the
+// largest, 1.2e-6 at the most, where bf16 keeps 3.9e-3.
 template <int kParts>
 __device__ __forceinline__ float grad_at(float x, float top, float factor)
 {
@@ -1436,8 +1438,10 @@ constexpr int64_t kLeastPiece = 2048;
 constexpr int64_t kMostPiece = 1ll << 20;     // keeps a tile's offsets below 2^32 bytes
 constexpr int64_t kBlocks = 256;              // that fill the device
 
-// Tiles of 256 x 256 up to which the statistics' are 64 x 64, since those leave most CUs idle: log-probabilities of 120 x 7616
-// x 4354, 30 of them, fp32 532 -> 125 us, bf16 117 -> 46; 1000 x 8000 x 1024, 128 of them, fp32 142 -> 131, but bf16 43 -> 53.
+// Tiles of 256 x 256 up to which the statistics' are 64 x 64, since those leave most CUs idle.  Log-probabilities of 250 x
+// 64 n x 1024, n a quarter of the tiles, in us by tiles of 256 and of 64: bf16 with 32 tiles 40 and 26, with 64 41 and 36, with
+// 96 41 and 48, with 256 51 and 109; fp32 136 and 47, 153 and 79, 181 and 107, 291 and 260.  With 4096 features, 500 x 8192
+// (64 tiles) bf16 89 and 72, fp32 496 and 253; 500 x 16384 101 and 162, 576 and 482.  So fp32 would gain up to 256 of them.
 constexpr int64_t kSmallTiles = 64;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -1612,7 +1616,7 @@ hipError_t launch_head(const HeadArgs& a, bool bf16, void* scratch, hipStream_t 
     if (a.tokens == 0) {
         if (a.loss) loss_kernel<<<1, kBlock, 0, stream>>>(nullptr, nullptr, a.loss);
         if ((e = hipGetLastError()) != hipSuccess || !a.dweight || a.accumulate) return e;
-        const int64_t values = a.vocab * a.cols;  // of which fp32 zeros cover two bf16 ones
+        const int64_t values = a.vocab * a.cols;
         if (!a.dweight_bf16) return launch_zero(static_cast<float*>(a.dweight), values, stream);
         return launch_zero_bf16(a.dweight, values, stream);
     }

@@ -94,8 +94,8 @@ def head(hidden, weight, labels, token_weight):
     # g: its logit's and sum's errors act on the softmax, then one rounding to the operands' type (three parts hold the 24
     # bits of an fp32 value).
     soft = c.abs()[:, None] * torch.exp(x - lse[:, None])
-    # With bf16 operands the exponentials that stay from the first pass are rounded to fp16 on the way: half a step of
-    # 2^-11, or of 2^-24 below its normal range.
+    # With bf16 operands the exponentials that stay from the first pass are kept in 16 bits on the way: 2^-11 of each, and
+    # for what is smaller than they reach far more than they lose (head_precision has the bounds that are relative to each).
     half = soft * 2.0 ** -11 + c.abs()[:, None] * 2.0 ** -25 if dtype == torch.bfloat16 else 0.0
     dg = half + soft * (dl[:, None] + 2.0 ** -20) + (g.abs() + soft * dl[:, None]) * HALF[dtype] + c.abs()[:, None] * 2 ** -22 * (soft > 0)
     ga = g.abs() + dg
